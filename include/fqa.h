@@ -381,6 +381,130 @@ FQA_API fqa_status fqa_e2m1_encode(const float* x, uint8_t* out, size_t npairs, 
  */
 FQA_API fqa_status fqa_exp2_error(float lo, float hi, uint32_t* max_rel_bits, void* cuda_stream);
 
+/* ------------------------------------------------------------------------
+ * Around the attention call: rotary positions, microscaled rows, their
+ * product.  These calls take zero rows, tokens or heads (nothing is launched)
+ * and define what non-finite inputs give, as stated at each.  [RTX-DE] SDPA
+ * quantization paragraph: the projections of Q, K and V are what the FP8 and
+ * FP4 schemes quantize; [KLEIN] section "왜 이런 차이가 나나": NVFP4 products
+ * on B200.  The pages give no formats' rules or positions' form; the readings
+ * are stated at each call.
+ */
+
+typedef enum {
+  FQA_DTYPE_BF16 = 0,       /* the first two as in fqa_out_dtype */
+  FQA_DTYPE_F32 = 1,
+  FQA_DTYPE_F16 = 2,
+  FQA_DTYPE_I32 = 3         /* positions only */
+} fqa_dtype;
+
+typedef enum {
+  FQA_MXFP8 = 0,            /* E4M3 elements, an E8M0 scale (2^(byte - 127)) per 32 */
+  FQA_MXFP4 = 1,            /* E2M1 elements, an E8M0 scale per 32 */
+  FQA_NVFP4 = 2             /* E2M1 elements, an E4M3 scale per 16, an FP32 scale per row */
+} fqa_mx_format;
+
+/*
+ * Microscaled rows [M, K] (M <= 2^24, K <= 2^20): K is padded with zeros to
+ * Kp = 32 ceil(K / 32).
+ *   codes      uint8 [M, Kp] (mxfp8) or [M, Kp / 2] (element 2i in the low
+ *              nibble of byte i), 16-byte aligned
+ *   scales     uint8 [ceil(M / 128)][ceil(Kp / W)][32][4][4], W = 128 (mxfp8,
+ *              mxfp4) or 64 (nvfp4) elements: the scale of row r and block j
+ *              at [r / 128][j / 4][r % 32][r / 32 % 4][j % 4], the order the
+ *              block-scaled tensor cores read; 16-byte aligned.  Scales of
+ *              blocks past Kp in a row's last word are 0; those of rows past
+ *              M are neither written nor used.
+ *   row_scale  FP32 [M], nvfp4 only (NULL otherwise)
+ * An element stands for code * scale (* row scale).
+ * The byte counts return 0 for invalid sizes (and for M = 0).
+ */
+FQA_API size_t fqa_mx_code_bytes(int M, int K, fqa_mx_format fmt);
+FQA_API size_t fqa_mx_scale_bytes(int M, int K, fqa_mx_format fmt);
+
+/*
+ * fqa_mx_quantize -- rows of BF16, FP16 or FP32 (row stride ldx >= 0 elements)
+ * -> microscaled rows.  Per block, amax = max |x|, everything round to nearest
+ * even:
+ *   mxfp8, mxfp4: the scale is the smallest power of two 2^e, e >= -127, with
+ *     amax <= L 2^e (L = 448 or 6: no element saturates), code = RN(x 2^-e);
+ *   nvfp4: the row scale is the smallest power of two 2^e, e >= -126, with
+ *     amax_row <= 2688 2^e; s = E4M3(fl32(amax 2^-e / 6)); code =
+ *     E2M1(x 2^-e / s), 0 where s = 0.
+ * A block (nvfp4: row) that holds a NaN or an infinity stands for NaN
+ * throughout: scale 0xFF (nvfp4: NaN row scale), codes 0.
+ */
+FQA_API fqa_status fqa_mx_quantize(const void* x, fqa_dtype dtype, int M, int K, int64_t ldx, fqa_mx_format fmt,
+                                   uint8_t* codes, uint8_t* scales, float* row_scale, void* cuda_stream);
+
+/*
+ * fqa_mx_rms_norm -- residual addition, RMS norm and quantization in one pass:
+ *   h = x + residual (FP32; h = x when residual is NULL)
+ *   residual_out = h, rounded to the residual's type
+ *   y = h / sqrt(mean of h^2 over the row + eps) * weight -> microscaled rows
+ * y is formed from h before its rounding.  weight and residual are FP32 or of
+ * x's type; residual_out is contiguous [M, K] and given exactly when residual
+ * is; it may be the residual itself (then ldr = K), or x where types and
+ * strides agree, and overlap nothing else.  eps >= 0.
+ */
+FQA_API fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t ldx, const void* weight,
+                                   fqa_dtype weight_dtype, float eps, const void* residual,
+                                   fqa_dtype residual_dtype, int64_t ldr, fqa_mx_format fmt, uint8_t* codes,
+                                   uint8_t* scales, float* row_scale, void* residual_out, void* cuda_stream);
+
+/*
+ * fqa_mx_dequantize -- microscaled rows -> the values they stand for, out
+ * [M, K] contiguous, rounded to out_dtype (code * scale is exact in FP32; the
+ * row scale's product is rounded to FP32 first).
+ */
+FQA_API fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int M,
+                                     int K, fqa_mx_format fmt, void* out, fqa_dtype out_dtype, void* cuda_stream);
+
+/*
+ * fqa_mx_matmul -- out[m, n] = sum over k of a[m, k] b[n, k] + bias[n] for
+ * microscaled A [M, K] and B [N, K] of one format (B: weights, one row per
+ * output feature), on the block-scaled tensor cores, accumulated in FP32,
+ * rounded once to out_dtype; out [M, N] contiguous.  bias: FP32 [N] or NULL.
+ * A row that stands for NaN gives NaN in its results only.  Results do not
+ * depend on anything but the inputs and sizes (K is split in a fixed order).
+ */
+FQA_API fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,
+                                 const uint8_t* b_codes, const uint8_t* b_scales, const float* b_row_scale,
+                                 const float* bias, int M, int N, int K, fqa_mx_format fmt, void* out,
+                                 fqa_dtype out_dtype, void* cuda_stream);
+
+/* Flags of fqa_rotary. */
+#define FQA_ROTARY_SPLIT 1    /* pair j = channels (j, D/2 + j); else (2j, 2j + 1) */
+#define FQA_ROTARY_SHARED 2   /* one spectrum over all axes; else one per axis */
+#define FQA_ROTARY_INVERSE 4  /* rotate back (the transpose, also the gradient's rotation) */
+
+/*
+ * fqa_rotary -- rotary positions over n_axes (1..4) axes for Q [B,Hq,N,128] and
+ * K [B,Hk,N,128], after a per-head RMS norm where a weight is given.
+ *   axes[a]: even channel counts, their sum D <= 128 (a multiple of 16 with
+ *     FQA_ROTARY_SPLIT); channels [D, 128) are not rotated.  Pairs are dealt
+ *     out to the axes in order, axes[a] / 2 to axis a.
+ *   angle of pair j on axis a = position[a] * theta^(-e); e = 2 i / axes[a] for
+ *     the i-th pair of its axis, or 2 j / D with FQA_ROTARY_SHARED
+ *   (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos), rounded once
+ *   norm: x / sqrt(mean of x^2 over the head's 128 channels + eps) * weight[128]
+ *     (of Q's type) before the rotation; NULL: none
+ * q, k       strides of batch, head and token in elements, channels adjacent
+ *            (a view of a packed projection will do); either may have no
+ *            heads.  Rows on 16-byte boundaries load in vectors.
+ * positions  int32 or FP32 [N, n_axes], contiguous; batch b starts positions_sb
+ *            elements after batch b - 1 (0: all batches alike)
+ * q_out, k_out  contiguous [B,H,N,128] of the inputs' type, 16-byte aligned; may
+ *            be q and k themselves where those are contiguous, and overlap
+ *            no other input.
+ * The angle is formed and reduced in FP64.
+ */
+FQA_API fqa_status fqa_rotary(const void* q, const void* k, fqa_dtype dtype, int B, int Hq, int Hk, int N, int d,
+                              int64_t q_sb, int64_t q_sh, int64_t q_sn, int64_t k_sb, int64_t k_sh, int64_t k_sn,
+                              const void* positions, fqa_dtype positions_dtype, int64_t positions_sb, int n_axes,
+                              const int* axes, double theta, int flags, const void* q_weight, const void* k_weight,
+                              float eps, void* q_out, void* k_out, void* cuda_stream);
+
 /*
  * fqa_e4m3_encode -- the library's binary32 -> E4M3 conversion (round to
  * nearest even, saturating to +-448, NaN -> 0x7F), exposed so that callers

@@ -12,6 +12,7 @@ or ``__graft_entry__.build()``); every call raises ImportError without it.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -22,6 +23,7 @@ LIB_PATH = os.path.join(_PKG, "libfqa.so")
 
 FQA_OK, FQA_ERR_INVALID_ARG, FQA_ERR_UNSUPPORTED, FQA_ERR_MISALIGNED, FQA_ERR_CUDA, FQA_ERR_TIMEOUT = range(6)
 FQA_OUT_BF16, FQA_OUT_F32 = 0, 1
+FQA_OUT_F16 = 2            # mx_matmul and mx_dequantize only
 HEAD_DIM = 128
 
 _lib = None
@@ -77,6 +79,21 @@ def _load():
     L.fqa_e2m1_encode.argtypes = [P, P, ctypes.c_size_t, P]
     L.fqa_exp2_error.restype = I
     L.fqa_exp2_error.argtypes = [ctypes.c_float, ctypes.c_float, P, P]
+    Z, Q = ctypes.c_size_t, ctypes.c_int64
+    for f in (L.fqa_mx_code_bytes, L.fqa_mx_scale_bytes):
+        f.restype = Z
+        f.argtypes = [I, I, I]
+    L.fqa_mx_quantize.restype = I
+    L.fqa_mx_quantize.argtypes = [P, I, I, I, Q, I, P, P, P, P]
+    L.fqa_mx_rms_norm.restype = I
+    L.fqa_mx_rms_norm.argtypes = [P, I, I, I, Q, P, I, ctypes.c_float, P, I, Q, I, P, P, P, P, P]
+    L.fqa_mx_dequantize.restype = I
+    L.fqa_mx_dequantize.argtypes = [P, P, P, I, I, I, P, I, P]
+    L.fqa_mx_matmul.restype = I
+    L.fqa_mx_matmul.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, I, P]
+    L.fqa_rotary.restype = I
+    L.fqa_rotary.argtypes = [P, P, I, I, I, I, I, I, Q, Q, Q, Q, Q, Q, P, I, Q, I, P, ctypes.c_double, I, P, P,
+                             ctypes.c_float, P, P, P]
     _lib = L
     return L
 
@@ -446,8 +463,11 @@ def attention_fp8_corrected(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q
 
 
 def fp8_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_scale: float,
-                  out_dtype: int = FQA_OUT_BF16, stream=None) -> torch.Tensor:
-    """The whole FP8 path: quantize, then fused FP8 attention."""
+                  out_dtype: int = FQA_OUT_BF16, stream=None, rot: Optional["Rotary"] = None) -> torch.Tensor:
+    """The whole FP8 path: with rot, rotary() on q and k (which may then be
+    strided views); quantize; fused FP8 attention."""
+    if rot is not None:
+        q, k = rotary(q, k, rot, stream=stream)
     return attention_fp8(quantize(q, k, v, stream=stream), softmax_scale, out_dtype, stream=stream)
 
 
@@ -516,9 +536,11 @@ def attention_nvfp4(qn: QuantizedNvfp4, qz: Quantized, softmax_scale: float, out
 
 
 def nvfp4_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_scale: float,
-                    out_dtype: int = FQA_OUT_BF16, stream=None) -> torch.Tensor:
-    """The whole FP4 Q.K path: quantize (V codes and the K mean), NVFP4 Q and
-    K, then the attention."""
+                    out_dtype: int = FQA_OUT_BF16, stream=None, rot: Optional["Rotary"] = None) -> torch.Tensor:
+    """The whole FP4 Q.K path: with rot, rotary() on q and k; quantize (V codes
+    and the K mean), NVFP4 Q and K, then the attention."""
+    if rot is not None:
+        q, k = rotary(q, k, rot, stream=stream)
     qz = quantize(q, k, v, stream=stream)
     return attention_nvfp4(quantize_nvfp4_qk(q, k, qz.k_mean, stream=stream), qz, softmax_scale, out_dtype,
                            stream=stream)
@@ -532,6 +554,366 @@ def e2m1_encode(x: torch.Tensor, stream=None) -> torch.Tensor:
     out = torch.empty(x.numel() // 2, dtype=torch.uint8, device=x.device)
     _check(fqa_e2m1_encode(x, out, stream=stream), "fqa_e2m1_encode")
     return out
+
+
+# ------------------------------------- rotary positions, microscaled rows
+
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2, torch.int32: 3}
+_OUT_DTYPE = {FQA_OUT_BF16: torch.bfloat16, FQA_OUT_F32: torch.float32, FQA_OUT_F16: torch.float16}
+MX_FORMATS = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
+_MX_MAX_ROWS, _MX_MAX_COLS = 1 << 24, 1 << 20
+
+
+class _on:
+    """The stream and device of a call: the tensors' device is made current and,
+    where a stream is given, outputs are allocated on it and the inputs marked
+    as used by it.  Gives the raw stream handle."""
+
+    __slots__ = ("stream", "context")
+
+    def __init__(self, device, stream, inputs):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream is None and device.index == torch.cuda.current_device():
+            self.stream, self.context = torch.cuda.current_stream(device), None
+            return
+        other = stream is not None and stream != torch.cuda.current_stream(device)
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.context = torch.cuda.stream(self.stream)
+        if other:
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _device_tensor(t, name: str, device=None) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+
+
+def _extent(t: torch.Tensor):
+    """First byte and the one past the last that the tensor's elements touch."""
+    n = 0 if t.numel() == 0 else sum((s - 1) * st for s, st in zip(t.shape, t.stride())) + 1
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+def _apart(out: torch.Tensor, name: str, inputs) -> None:
+    """Refuses an output that shares memory with one of the inputs."""
+    lo, hi = _extent(out)
+    for t in inputs:
+        if t is not None:
+            a, b = _extent(t)
+            if lo < b and a < hi:
+                raise ValueError(f"{name}: overlaps another tensor of the call")
+
+
+def _same_memory(a: torch.Tensor, b: torch.Tensor) -> bool:
+    return a.data_ptr() == b.data_ptr() and a.dtype == b.dtype and a.is_contiguous() and b.is_contiguous()
+
+
+def _float_dtype(t: torch.Tensor, name: str) -> int:
+    code = _DTYPE.get(t.dtype, 3)
+    if code == 3:
+        raise ValueError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+class Microscaled(NamedTuple):
+    """Rows of `cols` values in a microscaled format (MX_FORMATS), padded to a
+    multiple of 32: E4M3 codes with an E8M0 scale per 32 ("mxfp8"), E2M1 codes
+    with an E8M0 scale per 32 ("mxfp4"), or E2M1 codes with an E4M3 scale per 16
+    and a float32 scale per row ("nvfp4").  The layouts are those of
+    include/fqa.h; allocate with alloc_microscaled()."""
+    codes: torch.Tensor                  # uint8 [M, Kp], or [M, Kp / 2] for the 4-bit formats
+    scales: torch.Tensor                 # uint8 [ceil(M/128), words, 32, 4, 4]
+    row_scale: Optional[torch.Tensor]    # float32 [M], nvfp4 only
+    cols: int
+    fmt: str
+
+
+def _mx_format(fmt) -> int:
+    code = MX_FORMATS.get(fmt) if isinstance(fmt, str) else None
+    if code is None:
+        raise ValueError(f"fmt: expected one of {', '.join(MX_FORMATS)}, got {fmt!r}")
+    return code
+
+
+def _mx_shapes(M: int, K: int, code: int):
+    """Shapes of the codes and of the scale tiles of [M, K]."""
+    if not 0 <= M <= _MX_MAX_ROWS or not 1 <= K <= _MX_MAX_COLS:
+        raise ValueError(f"[{M}, {K}]: microscaled rows are at most 2^24, of 1 to 2^20 values")
+    kp = (K + 31) // 32 * 32
+    width = 64 if code == 2 else 128
+    return (M, kp if code == 0 else kp // 2), ((M + 127) // 128, (kp + width - 1) // width, 32, 4, 4)
+
+
+def alloc_microscaled(M: int, K: int, fmt: str, device) -> Microscaled:
+    code = _mx_format(fmt)
+    codes, scales = _mx_shapes(M, K, code)
+    return Microscaled(torch.empty(codes, dtype=torch.uint8, device=device),
+                       torch.empty(scales, dtype=torch.uint8, device=device),
+                       torch.empty(M, dtype=torch.float32, device=device) if code == 2 else None, K, fmt)
+
+
+def _require_microscaled(q, name: str, device=None):
+    """(rows, format code) of a checked Microscaled."""
+    if not isinstance(q, Microscaled):
+        raise TypeError(f"{name}: expected a Microscaled, got {type(q).__name__}")
+    code = _mx_format(q.fmt)
+    _device_tensor(q.codes, f"{name}.codes", device)
+    device = q.codes.device
+    if q.codes.dim() != 2:
+        raise ValueError(f"{name}.codes: expected a 2-D tensor")
+    M = q.codes.shape[0]
+    codes, scales = _mx_shapes(M, q.cols, code)
+    parts = [(q.codes, "codes", torch.uint8, codes), (q.scales, "scales", torch.uint8, scales)]
+    if code == 2:
+        parts.append((q.row_scale, "row_scale", torch.float32, (M,)))
+    elif q.row_scale is not None:
+        raise ValueError(f"{name}.row_scale: {q.fmt} rows have none")
+    for t, part, dtype, shape in parts:
+        _device_tensor(t, f"{name}.{part}", device)
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}.{part}: expected a contiguous {dtype} tensor of shape {shape}, "
+                             f"got {t.dtype} {tuple(t.shape)}")
+    return M, code
+
+
+def _rows(x, name: str):
+    """(rows, row length, row stride) of a tensor [..., K] with adjacent channels."""
+    if x.dim() < 2:
+        raise ValueError(f"{name}: expected [..., K] with at least two dimensions, got {tuple(x.shape)}")
+    if x.dim() > 2:
+        try:
+            x = x.view(-1, x.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{name}: the leading dimensions have no common row stride") from None
+    M, K = x.shape
+    if K > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: expected adjacent channels, got stride {x.stride(1)}")
+    return M, K, x.stride(0) if M > 1 else K
+
+
+def mx_quantize(x: torch.Tensor, fmt: str, out: Optional[Microscaled] = None, stream=None) -> Microscaled:
+    """Rows [..., K] of bfloat16, float16 or float32 -> Microscaled rows (leading
+    dimensions flattened).  A block (nvfp4: a row) with a NaN or an infinity
+    stands for NaN."""
+    _device_tensor(x, "x")
+    dtype, code = _float_dtype(x, "x"), _mx_format(fmt)
+    M, K, ld = _rows(x, "x")
+    _mx_shapes(M, K, code)
+    if out is not None:
+        if _require_microscaled(out, "out", x.device) != (M, code) or out.cols != K:
+            raise ValueError(f"out: expected {fmt} rows [{M}, {K}]")
+        for t in out[:3]:
+            if t is not None:
+                _apart(t, "out", (x,))
+    with _on(x.device, stream, (x,)) as s:
+        if out is None:
+            out = alloc_microscaled(M, K, fmt, x.device)
+        _check(_load().fqa_mx_quantize(x.data_ptr(), dtype, M, K, ld, code, out.codes.data_ptr(),
+                                       out.scales.data_ptr(), _at(out.row_scale), s), "fqa_mx_quantize")
+    return out
+
+
+def mx_dequantize(q: Microscaled, out_dtype: int = FQA_OUT_BF16, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """The values that microscaled rows stand for, [M, cols]."""
+    M, code = _require_microscaled(q, "q")
+    dt = _OUT_DTYPE.get(out_dtype)
+    if dt is None:
+        raise ValueError(f"out_dtype: unknown value {out_dtype!r}")
+    device = q.codes.device
+    if out is not None:
+        _device_tensor(out, "out", device)
+        _require(out, dt, "out", (M, q.cols))
+        _apart(out, "out", q[:3])
+    with _on(device, stream, q[:3]) as s:
+        if out is None:
+            out = torch.empty(M, q.cols, dtype=dt, device=device)
+        _check(_load().fqa_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), _at(q.row_scale), M, q.cols, code,
+                                         out.data_ptr(), out_dtype, s), "fqa_mx_dequantize")
+    return out
+
+
+def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, fmt: str = "mxfp8", residual: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, out: Optional[Microscaled] = None, residual_out: Optional[torch.Tensor] = None,
+                stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over the rows of
+    [..., K]: (y as Microscaled rows, h in residual's type, or None without a
+    residual).  weight [K] and residual are of x's type or float32.
+    residual_out may be residual itself (or x, where of the same type)."""
+    _device_tensor(x, "x")
+    dtype, code = _float_dtype(x, "x"), _mx_format(fmt)
+    M, K, ld = _rows(x, "x")
+    _mx_shapes(M, K, code)
+    _device_tensor(weight, "weight", x.device)
+    _require(weight, torch.float32 if weight.dtype == torch.float32 else x.dtype, "weight", (K,))
+    ldr = K
+    if residual is not None:
+        _device_tensor(residual, "residual", x.device)
+        if residual.shape != x.shape or residual.dtype not in (x.dtype, torch.float32):
+            raise ValueError(f"residual: expected {tuple(x.shape)} of {x.dtype} or float32, "
+                             f"got {tuple(residual.shape)} {residual.dtype}")
+        ldr = _rows(residual, "residual")[2]
+        if residual_out is not None:
+            _device_tensor(residual_out, "residual_out", x.device)
+            _require(residual_out, residual.dtype, "residual_out", x.shape)
+            _apart(residual_out, "residual_out",
+                   [weight] + [t for t in (x, residual) if not _same_memory(residual_out, t)])
+    elif residual_out is not None:
+        raise ValueError("residual_out: there is no residual")
+    if not 0.0 <= eps < float("inf"):
+        raise ValueError(f"eps: expected a finite value of at least 0, got {eps}")
+    if out is not None:
+        if _require_microscaled(out, "out", x.device) != (M, code) or out.cols != K:
+            raise ValueError(f"out: expected {fmt} rows [{M}, {K}]")
+        for t in out[:3]:
+            if t is not None:
+                _apart(t, "out", (x, weight, residual, residual_out))
+    with _on(x.device, stream, (x, weight, residual)) as s:
+        if out is None:
+            out = alloc_microscaled(M, K, fmt, x.device)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+        _check(_load().fqa_mx_rms_norm(
+            x.data_ptr(), dtype, M, K, ld, weight.data_ptr(), _DTYPE[weight.dtype], eps, _at(residual),
+            dtype if residual is None else _DTYPE[residual.dtype], ldr, code, out.codes.data_ptr(),
+            out.scales.data_ptr(), _at(out.row_scale), _at(residual_out), s), "fqa_mx_rms_norm")
+    return out, residual_out
+
+
+def mx_matmul(a: Microscaled, b: Microscaled, bias: Optional[torch.Tensor] = None, out_dtype: int = FQA_OUT_BF16,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """a [M, K] times the transpose of b [N, K] (a projection's weights), both
+    microscaled rows of one format, plus a float32 bias [N]: [M, N]."""
+    M, code = _require_microscaled(a, "a")
+    device = a.codes.device
+    N, other = _require_microscaled(b, "b", device)
+    if other != code or a.cols != b.cols:
+        raise ValueError(f"a and b: {a.fmt} rows of {a.cols} against {b.fmt} rows of {b.cols}")
+    dt = _OUT_DTYPE.get(out_dtype)
+    if dt is None:
+        raise ValueError(f"out_dtype: unknown value {out_dtype!r}")
+    if bias is not None:
+        _device_tensor(bias, "bias", device)
+        _require(bias, torch.float32, "bias", (N,))
+    if out is not None:
+        _device_tensor(out, "out", device)
+        _require(out, dt, "out", (M, N))
+        _apart(out, "out", (*a[:3], *b[:3], bias))
+    with _on(device, stream, (*a[:3], *b[:3], bias)) as s:
+        if out is None:
+            out = torch.empty(M, N, dtype=dt, device=device)
+        _check(_load().fqa_mx_matmul(a.codes.data_ptr(), a.scales.data_ptr(), _at(a.row_scale), b.codes.data_ptr(),
+                                     b.scales.data_ptr(), _at(b.row_scale), _at(bias), M, N, a.cols, code,
+                                     out.data_ptr(), out_dtype, s), "fqa_mx_matmul")
+    return out
+
+
+class Rotary(NamedTuple):
+    """Rotary positions for rotary() and the attention paths: positions int32 or
+    float32 [N, A] or [B, N, A] for A axes (1..4), axes the channels of each
+    (even, together at most 128; the rest is not rotated).  `split` pairs
+    channels (j, D/2 + j) instead of (2j, 2j + 1), D = sum(axes), then a multiple
+    of 16; `shared` takes one spectrum theta^(-2j/D) over all axes instead of
+    theta^(-2i/axes[a]) on each.  q_weight and k_weight [128] (of q's type): RMS
+    norm of each head before the rotation."""
+    positions: torch.Tensor
+    axes: tuple
+    theta: float = 10000.0
+    split: bool = False
+    shared: bool = False
+    q_weight: Optional[torch.Tensor] = None
+    k_weight: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+
+
+@functools.lru_cache(maxsize=64)
+def _axes_array(axes: tuple, split: bool):
+    if not 1 <= len(axes) <= 4 or any(not isinstance(a, int) or a < 2 or a % 2 for a in axes) or sum(axes) > HEAD_DIM:
+        raise ValueError(f"axes: expected one to four even channel counts, together at most {HEAD_DIM}, got {axes}")
+    if split and sum(axes) % 16:
+        raise ValueError(f"axes: split pairs need a multiple of 16 channels, got {sum(axes)}")
+    return (ctypes.c_int * len(axes))(*axes)
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary, inverse: bool = False,
+           q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Q [B,Hq,N,128] and K [B,Hk,N,128] (any strides over batch, heads and tokens,
+    adjacent channels; k may be None) -> both normalized (where rot has
+    weights) and rotated, contiguous.  `inverse` rotates back.  An output may be
+    its own input where that is contiguous."""
+    _device_tensor(q, "q")
+    device, dtype = q.device, _float_dtype(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q: expected a [B, H, N, 128] tensor")
+    B, Hq, N, d = q.shape
+    Hk = 0
+    if k is not None:
+        _device_tensor(k, "k", device)
+        if k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+            raise ValueError(f"k: expected [{B}, H, {N}, {d}] of {q.dtype}, got {tuple(k.shape)} {k.dtype}")
+        Hk = k.shape[1]
+    elif k_out is not None:
+        raise ValueError("k_out: there is no k")
+    if d != HEAD_DIM:
+        raise ValueError(f"q: expected {HEAD_DIM} channels, got {d}")
+    for name, t in (("q", q), ("k", k)):
+        if t is not None and t.stride(3) != 1:
+            raise ValueError(f"{name}: expected adjacent channels, got stride {t.stride(3)}")
+    if not isinstance(rot, Rotary):
+        raise TypeError(f"rot: expected a Rotary, got {type(rot).__name__}")
+    axes = _axes_array(tuple(rot.axes), bool(rot.split))
+    pos, A = rot.positions, len(rot.axes)
+    _device_tensor(pos, "rot.positions", device)
+    if pos.dtype not in (torch.int32, torch.float32) or not pos.is_contiguous() or (
+            pos.shape != (N, A) and pos.shape != (B, N, A) and pos.shape != (1, N, A)):
+        raise ValueError(f"rot.positions: expected contiguous int32 or float32 [{N}, {A}] or [{B}, {N}, {A}], "
+                         f"got {pos.dtype} {tuple(pos.shape)}")
+    for name, w in (("rot.q_weight", rot.q_weight), ("rot.k_weight", rot.k_weight)):
+        if w is not None:
+            _device_tensor(w, name, device)
+            _require(w, q.dtype, name, (HEAD_DIM,))
+    if not 0.0 < rot.theta < float("inf") or not 0.0 <= rot.eps < float("inf"):
+        raise ValueError(f"rot: expected a finite theta > 0 and eps >= 0, got {rot.theta} and {rot.eps}")
+    inputs = (q, k, pos, rot.q_weight, rot.k_weight)
+    for name, o, own, others in (("q_out", q_out, q, inputs[1:]), ("k_out", k_out, k, (q, *inputs[2:]))):
+        if o is not None:
+            _device_tensor(o, name, device)
+            _require(o, q.dtype, name, own.shape)
+            _apart(o, name, others if _same_memory(o, own) else (own, *others))
+    if q_out is not None and k_out is not None:
+        _apart(k_out, "k_out", (q_out,))
+    with _on(device, stream, inputs) as s:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=device)
+        ks = (0, 0, 0) if k is None else k.stride()[:3]
+        _check(_load().fqa_rotary(
+            q.data_ptr(), _at(k), dtype, B, Hq, Hk, N, d, *q.stride()[:3], *ks, pos.data_ptr(), _DTYPE[pos.dtype],
+            N * A if pos.dim() == 3 and pos.shape[0] > 1 else 0, A, axes, rot.theta,
+            (1 if rot.split else 0) | (2 if rot.shared else 0) | (4 if inverse else 0), _at(rot.q_weight),
+            _at(rot.k_weight), rot.eps, q_out.data_ptr(), _at(k_out), s), "fqa_rotary")
+    return q_out, k_out
 
 
 def softmax_scale(d: int = HEAD_DIM) -> float:

@@ -1,6 +1,7 @@
 // fqa.cu -- the library's C ABI (include/fqa.h): host-side argument checks,
 // TMA tensor-map encoding and kernel launches.  One translation unit holds
 // every kernel, so the device status word needs no relocatable device code.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -16,14 +17,19 @@
 #include "attention_ws.cuh"
 #include "correct.cuh"
 #include "device.cuh"
+#include "matmul_mx.cuh"
+#include "microscale.cuh"
 #include "quantize.cuh"
 #include "quantize_nvfp4.cuh"
+#include "rotary.cuh"
 
 namespace fqa {
 
 __device__ uint32_t g_status_word;
 
 constexpr int kMaxDevices = 64;
+constexpr int64_t kMxMaxRows = 1 << 24;    // rows and columns of a microscaled operand
+constexpr int kMxMaxCols = 1 << 20;
 
 // Per-device lookups, cached only once they succeed: a failed first call
 // (e.g. one made while a stream is being captured) is retried by the next.
@@ -111,6 +117,22 @@ static bool make_tmap_fp4(CUtensorMap* m, const void* base, int N, int heads) {
   return r == CUDA_SUCCESS;
 }
 
+// 2-D view (byte, row) of rows of codes, row_bytes a multiple of 16; box = 128
+// bytes x box_rows rows, 128-byte swizzle.  Bytes and rows past the end read
+// as zeros.
+static bool make_tmap_rows(CUtensorMap* m, const void* base, int row_bytes, int rows, int box_rows) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Shape checks shared by every call: any N >= 1 (the last 64-token block and
@@ -184,6 +206,97 @@ static fqa_status launch_attention_fp8(const void* q, const void* k, const void*
   const int grid = items < sms ? items : sms;
   fn<<<grid, kF8Threads, F8Traits::kSmemBytes, stream>>>(tq, tk, tv, prm);
   return launch_status();
+}
+
+// -------------------------------------------- launches of microscaled rows
+
+// One launch of the row kernel that fits the row: 8 elements a thread and
+// chunk, up to four chunks in registers.  Threads per row by K: a warp up to
+// 1024 elements (no block-wide sums), 128 up to 4096, 512 up to 16384, and
+// longer rows are read again for each step.
+template <typename T, int FMT, bool kNorm>
+static void launch_mx_rows(const MxRowParams& p, cudaStream_t s) {
+  const int width = p.KT * MxTraits<FMT>::kWordChunks * 8;
+  if (width <= 1024)
+    mx_row_kernel<T, FMT, kNorm, 32, 4, false><<<(p.M + 3) / 4, 128, 0, s>>>(p);
+  else if (width <= 4096)
+    mx_row_kernel<T, FMT, kNorm, 128, 4, false><<<p.M, 128, 0, s>>>(p);
+  else if (width <= 16384)
+    mx_row_kernel<T, FMT, kNorm, 512, 4, false><<<p.M, 512, 0, s>>>(p);
+  else
+    mx_row_kernel<T, FMT, kNorm, 512, 1, true><<<p.M, 512, 0, s>>>(p);
+}
+
+template <typename T, bool kNorm>
+static void launch_mx_format(const MxRowParams& p, int fmt, cudaStream_t s) {
+  if (fmt == FQA_MXFP8)
+    launch_mx_rows<T, kMxFp8, kNorm>(p, s);
+  else if (fmt == FQA_MXFP4)
+    launch_mx_rows<T, kMxFp4, kNorm>(p, s);
+  else
+    launch_mx_rows<T, kNvFp4, kNorm>(p, s);
+}
+
+template <bool kNorm>
+static fqa_status launch_mx(const MxRowParams& p, int dtype, int fmt, cudaStream_t s) {
+  if (dtype == FQA_DTYPE_BF16)
+    launch_mx_format<__nv_bfloat16, kNorm>(p, fmt, s);
+  else if (dtype == FQA_DTYPE_F16)
+    launch_mx_format<__half, kNorm>(p, fmt, s);
+  else
+    launch_mx_format<float, kNorm>(p, fmt, s);
+  return launch_status();
+}
+
+template <typename T>
+static void launch_mx_dequantize(const MxDequantParams& p, int fmt, cudaStream_t s) {
+  const int64_t chunks = (int64_t)p.M * ((p.K + 7) / 8);
+  const int grid = (int)std::min<int64_t>((chunks + 255) / 256, 148 * 64);
+  if (fmt == FQA_MXFP8)
+    mx_dequantize_kernel<T, kMxFp8><<<grid, 256, 0, s>>>(p);
+  else if (fmt == FQA_MXFP4)
+    mx_dequantize_kernel<T, kMxFp4><<<grid, 256, 0, s>>>(p);
+  else
+    mx_dequantize_kernel<T, kNvFp4><<<grid, 256, 0, s>>>(p);
+}
+
+template <int FMT, int NT>
+static fqa_status launch_mx_small(const uint8_t* a, const uint8_t* b, const MxMatmulParams& p, int row_bytes,
+                                  cudaStream_t s) {
+  using T = MxSmall<FMT, NT>;
+  CUtensorMap tp, tq;
+  if (!make_tmap_rows(&tp, b, row_bytes, p.N, 128) || !make_tmap_rows(&tq, a, row_bytes, p.M, NT)) return FQA_ERR_CUDA;
+  const int64_t tiles = (int64_t)((p.N + 127) / 128) * ((p.M + NT - 1) / NT);
+  // split K while the CTAs stay within two per SM and each keeps two stages
+  const int stages = (p.mmas + 3) / 4;
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks * 2 <= 2 * num_sms() && stages >= 4 * ranks) ranks *= 2;
+  if (tiles * ranks > INT32_MAX) return FQA_ERR_UNSUPPORTED;
+  const auto fn = mx_matmul_small_kernel<FMT, NT>;
+  if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess)
+    return FQA_ERR_CUDA;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * ranks));
+  cfg.blockDim = dim3(kMxSmallThreads);
+  cfg.dynamicSmemBytes = T::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, tp, tq, p, ranks) != cudaSuccess) return FQA_ERR_CUDA;
+  return launch_status();
+}
+
+template <int FMT>
+static fqa_status launch_mx_matmul(const uint8_t* a, const uint8_t* b, const MxMatmulParams& p, int row_bytes,
+                                   cudaStream_t s) {
+  if (p.M <= 16) return launch_mx_small<FMT, 16>(a, b, p, row_bytes, s);
+  if (p.M <= 32) return launch_mx_small<FMT, 32>(a, b, p, row_bytes, s);
+  if (p.M <= 64) return launch_mx_small<FMT, 64>(a, b, p, row_bytes, s);
+  return launch_mx_small<FMT, 128>(a, b, p, row_bytes, s);
 }
 
 }  // namespace fqa
@@ -569,6 +682,229 @@ fqa_status fqa_attention_nvfp4(const uint8_t* q4, const uint8_t* k4, const uint8
   if (sms <= 0) return FQA_ERR_CUDA;
   const int grid = items < sms ? items : sms;
   fn<<<grid, kNvThreads, NvTraits::kSmemBytes, static_cast<cudaStream_t>(cuda_stream)>>>(tq, tk, tv, prm);
+  return launch_status();
+}
+
+// ------------------------------------------------- microscaled rows
+
+static bool mx_shape_ok(int64_t rows, int K) { return rows >= 0 && rows <= kMxMaxRows && K >= 1 && K <= kMxMaxCols; }
+static bool mx_format_ok(int fmt) { return fmt == FQA_MXFP8 || fmt == FQA_MXFP4 || fmt == FQA_NVFP4; }
+static bool dtype_ok(int t) { return t == FQA_DTYPE_BF16 || t == FQA_DTYPE_F32 || t == FQA_DTYPE_F16; }
+static size_t dtype_bytes(int t) { return t == FQA_DTYPE_F32 ? 4 : 2; }
+static int mx_padded(int K) { return (K + 31) / 32 * 32; }
+static int mx_words(int K, int fmt) { return (mx_padded(K) + 4 * mx_block(fmt) - 1) / (4 * mx_block(fmt)); }
+
+size_t fqa_mx_code_bytes(int M, int K, fqa_mx_format fmt) {
+  if (!mx_format_ok(fmt) || !mx_shape_ok(M, K)) return 0;
+  return (size_t)M * (mx_padded(K) / mx_per_byte(fmt));
+}
+
+size_t fqa_mx_scale_bytes(int M, int K, fqa_mx_format fmt) {
+  if (!mx_format_ok(fmt) || !mx_shape_ok(M, K)) return 0;
+  return (size_t)((M + 127) / 128) * mx_words(K, fmt) * 512;
+}
+
+// Rows whose every start is 16-byte aligned and whose length is whole chunks.
+static bool rows_vectorize(const void* base, int64_t ld, int K, size_t elt) {
+  return K % 8 == 0 && aligned(base, 16) && (ld * (int64_t)elt) % 16 == 0;
+}
+
+// The checks and fields common to both row calls.
+static fqa_status mx_row_params(MxRowParams* p, const void* x, int dtype, int M, int K, int64_t ldx, int fmt,
+                                uint8_t* codes, uint8_t* scales, float* row_scale) {
+  if (!dtype_ok(dtype) || !mx_format_ok(fmt) || M < 0 || K < 1) return FQA_ERR_INVALID_ARG;
+  if (!mx_shape_ok(M, K)) return FQA_ERR_UNSUPPORTED;
+  if (M == 0) return FQA_OK;
+  if (x == nullptr || codes == nullptr || scales == nullptr || ldx < 0) return FQA_ERR_INVALID_ARG;
+  if (fmt == FQA_NVFP4 && row_scale == nullptr) return FQA_ERR_INVALID_ARG;
+  const size_t elt = dtype_bytes(dtype);
+  if (!aligned(x, elt) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(row_scale, 4))
+    return FQA_ERR_MISALIGNED;
+  *p = MxRowParams{};
+  p->x = x;
+  p->ldx = ldx;
+  p->M = M;
+  p->K = K;
+  p->Kp = mx_padded(K);
+  p->KT = mx_words(K, fmt);
+  p->vec_x = rows_vectorize(x, ldx, K, elt);
+  p->codes = codes;
+  p->scales = reinterpret_cast<uint32_t*>(scales);
+  p->row_scale = row_scale;
+  return FQA_OK;
+}
+
+fqa_status fqa_mx_quantize(const void* x, fqa_dtype dtype, int M, int K, int64_t ldx, fqa_mx_format fmt,
+                           uint8_t* codes, uint8_t* scales, float* row_scale, void* cuda_stream) {
+  MxRowParams p;
+  const fqa_status st = mx_row_params(&p, x, dtype, M, K, ldx, fmt, codes, scales, row_scale);
+  if (st != FQA_OK || M == 0) return st;
+  return launch_mx<false>(p, dtype, fmt, static_cast<cudaStream_t>(cuda_stream));
+}
+
+fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t ldx, const void* weight,
+                           fqa_dtype weight_dtype, float eps, const void* residual, fqa_dtype residual_dtype,
+                           int64_t ldr, fqa_mx_format fmt, uint8_t* codes, uint8_t* scales, float* row_scale,
+                           void* residual_out, void* cuda_stream) {
+  MxRowParams p;
+  const fqa_status st = mx_row_params(&p, x, dtype, M, K, ldx, fmt, codes, scales, row_scale);
+  if (st != FQA_OK) return st;
+  if (!(std::isfinite(eps) && eps >= 0.0f)) return FQA_ERR_INVALID_ARG;
+  if (weight_dtype != dtype && weight_dtype != FQA_DTYPE_F32) return FQA_ERR_INVALID_ARG;
+  const bool res = residual != nullptr;
+  if (res && residual_dtype != dtype && residual_dtype != FQA_DTYPE_F32) return FQA_ERR_INVALID_ARG;
+  if (M == 0) return FQA_OK;
+  if (weight == nullptr || res != (residual_out != nullptr) || (res && ldr < 0)) return FQA_ERR_INVALID_ARG;
+  const size_t welt = dtype_bytes(weight_dtype), relt = dtype_bytes(residual_dtype);
+  if (!aligned(weight, welt) || (res && (!aligned(residual, relt) || !aligned(residual_out, relt))))
+    return FQA_ERR_MISALIGNED;
+  p.weight = weight;
+  p.w_f32 = weight_dtype == FQA_DTYPE_F32;
+  p.vec_w = rows_vectorize(weight, 0, K, welt);
+  p.eps = eps;
+  p.residual = residual;
+  p.residual_out = residual_out;
+  if (res) {
+    p.ldr = ldr;
+    p.res_f32 = residual_dtype == FQA_DTYPE_F32;
+    p.vec_r = rows_vectorize(residual, ldr, K, relt);
+    p.vec_o = rows_vectorize(residual_out, K, K, relt);
+  }
+  return launch_mx<true>(p, dtype, fmt, static_cast<cudaStream_t>(cuda_stream));
+}
+
+fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int M, int K,
+                             fqa_mx_format fmt, void* out, fqa_dtype out_dtype, void* cuda_stream) {
+  if (!mx_format_ok(fmt) || !dtype_ok(out_dtype) || M < 0 || K < 1) return FQA_ERR_INVALID_ARG;
+  if (!mx_shape_ok(M, K)) return FQA_ERR_UNSUPPORTED;
+  if (M == 0) return FQA_OK;
+  if (codes == nullptr || scales == nullptr || out == nullptr) return FQA_ERR_INVALID_ARG;
+  if (fmt == FQA_NVFP4 && row_scale == nullptr) return FQA_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(row_scale, 4) || !aligned(out, dtype_bytes(out_dtype)))
+    return FQA_ERR_MISALIGNED;
+  MxDequantParams p{codes, scales, row_scale, out, M, K, mx_padded(K), mx_words(K, fmt),
+                    rows_vectorize(out, K, K, dtype_bytes(out_dtype))};
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (out_dtype == FQA_DTYPE_BF16)
+    launch_mx_dequantize<__nv_bfloat16>(p, fmt, s);
+  else if (out_dtype == FQA_DTYPE_F16)
+    launch_mx_dequantize<__half>(p, fmt, s);
+  else
+    launch_mx_dequantize<float>(p, fmt, s);
+  return launch_status();
+}
+
+fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,
+                         const uint8_t* b_codes, const uint8_t* b_scales, const float* b_row_scale,
+                         const float* bias, int M, int N, int K, fqa_mx_format fmt, void* out, fqa_dtype out_dtype,
+                         void* cuda_stream) {
+  if (!mx_format_ok(fmt) || !dtype_ok(out_dtype) || M < 0 || N < 0 || K < 1) return FQA_ERR_INVALID_ARG;
+  if (!mx_shape_ok(M, K) || !mx_shape_ok(N, K)) return FQA_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return FQA_OK;
+  const void* ptrs[] = {a_codes, a_scales, b_codes, b_scales, out};
+  for (const void* q : ptrs)
+    if (q == nullptr) return FQA_ERR_INVALID_ARG;
+  if (fmt == FQA_NVFP4 && (a_row_scale == nullptr || b_row_scale == nullptr)) return FQA_ERR_INVALID_ARG;
+  const void* a16[] = {a_codes, a_scales, b_codes, b_scales};
+  for (const void* q : a16)
+    if (!aligned(q, 16)) return FQA_ERR_MISALIGNED;
+  const void* a4[] = {a_row_scale, b_row_scale, bias};
+  for (const void* q : a4)
+    if (!aligned(q, 4)) return FQA_ERR_MISALIGNED;
+  if (!aligned(out, dtype_bytes(out_dtype))) return FQA_ERR_MISALIGNED;
+  fqa_status st = FQA_OK;
+  uint32_t* status = status_ptr(&st);
+  if (!status) return st;
+  const int row_bytes = mx_padded(K) / mx_per_byte(fmt);
+  const bool nv = fmt == FQA_NVFP4;
+  const MxMatmulParams p{a_scales, b_scales, nv ? a_row_scale : nullptr, nv ? b_row_scale : nullptr, bias, out, M, N,
+                         (row_bytes + 31) / 32, mx_words(K, fmt), (int)out_dtype, status};
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (fmt == FQA_MXFP8) return launch_mx_matmul<kMxFp8>(a_codes, b_codes, p, row_bytes, s);
+  if (fmt == FQA_MXFP4) return launch_mx_matmul<kMxFp4>(a_codes, b_codes, p, row_bytes, s);
+  return launch_mx_matmul<kNvFp4>(a_codes, b_codes, p, row_bytes, s);
+}
+
+// ------------------------------------------------------------- rotary
+
+fqa_status fqa_rotary(const void* q, const void* k, fqa_dtype dtype, int B, int Hq, int Hk, int N, int d,
+                      int64_t q_sb, int64_t q_sh, int64_t q_sn, int64_t k_sb, int64_t k_sh, int64_t k_sn,
+                      const void* positions, fqa_dtype positions_dtype, int64_t positions_sb, int n_axes,
+                      const int* axes, double theta, int flags, const void* q_weight, const void* k_weight, float eps,
+                      void* q_out, void* k_out, void* cuda_stream) {
+  if (!dtype_ok(dtype) || B < 0 || N < 0 || Hq < 0 || Hk < 0) return FQA_ERR_INVALID_ARG;
+  if (d != kHeadDim) return FQA_ERR_UNSUPPORTED;
+  if (positions_dtype != FQA_DTYPE_I32 && positions_dtype != FQA_DTYPE_F32) return FQA_ERR_INVALID_ARG;
+  if (n_axes < 1 || axes == nullptr || (flags & ~(FQA_ROTARY_SPLIT | FQA_ROTARY_SHARED | FQA_ROTARY_INVERSE)) != 0)
+    return FQA_ERR_INVALID_ARG;
+  if (n_axes > kRotMaxAxes) return FQA_ERR_UNSUPPORTED;
+  if (!(std::isfinite(theta) && theta > 0.0) || !(std::isfinite(eps) && eps >= 0.0f)) return FQA_ERR_INVALID_ARG;
+  int width = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (axes[a] < 2 || axes[a] % 2 != 0 || axes[a] > kHeadDim) return FQA_ERR_INVALID_ARG;
+    width += axes[a];
+  }
+  const bool split = flags & FQA_ROTARY_SPLIT;
+  if (width > kHeadDim) return FQA_ERR_INVALID_ARG;
+  if (split && width % 16 != 0) return FQA_ERR_UNSUPPORTED;
+  if ((int64_t)B * N >= (int64_t(1) << 31) || (int64_t)Hq + Hk > 65535) return FQA_ERR_UNSUPPORTED;
+  const int total = Hq + Hk;
+  if (B == 0 || N == 0 || total == 0) return FQA_OK;
+  if (positions == nullptr || positions_sb < 0) return FQA_ERR_INVALID_ARG;
+  if ((Hq > 0 && (q == nullptr || q_out == nullptr)) || (Hk > 0 && (k == nullptr || k_out == nullptr)))
+    return FQA_ERR_INVALID_ARG;
+  const size_t elt = dtype_bytes(dtype);
+  if (!aligned(positions, 4) || !aligned(q_out, 16) || !aligned(k_out, 16)) return FQA_ERR_MISALIGNED;
+  const void* ae[] = {q, k, q_weight, k_weight};
+  for (const void* ptr : ae)
+    if (!aligned(ptr, elt)) return FQA_ERR_MISALIGNED;
+  RotaryParams p{};
+  const int64_t strides[2][3] = {{q_sb, q_sh, q_sn}, {k_sb, k_sh, k_sn}};
+  const void* in[2] = {q, k};
+  for (int i = 0; i < 2; ++i) {
+    p.in[i] = in[i];
+    p.sb[i] = strides[i][0];
+    p.sh[i] = strides[i][1];
+    p.sn[i] = strides[i][2];
+    p.vec[i] = aligned(in[i], 16);
+    for (int64_t s : strides[i]) p.vec[i] = p.vec[i] && (s * (int64_t)elt) % 16 == 0;
+  }
+  p.out[0] = q_out;
+  p.out[1] = k_out;
+  p.weight[0] = q_weight;
+  p.weight[1] = k_weight;
+  p.heads[0] = Hq;
+  p.heads[1] = Hk;
+  p.pos = positions;
+  p.pos_sb = positions_sb;
+  p.pos_f32 = positions_dtype == FQA_DTYPE_F32;
+  p.n_axes = n_axes;
+  p.B = B;
+  p.N = N;
+  p.pairs = width / 2;
+  p.eps = eps;
+  p.sign = (flags & FQA_ROTARY_INVERSE) ? -1.0f : 1.0f;
+  for (int a = 0, j = 0; a < n_axes; ++a)
+    for (int i = 0; i < axes[a] / 2; ++i, ++j) {
+      const double e = (flags & FQA_ROTARY_SHARED) ? 2.0 * j / width : 2.0 * i / axes[a];
+      p.f[j] = std::pow(theta, -e) / 6.283185307179586476925;
+      p.axis[j] = (uint8_t)a;
+    }
+  // groups of 16 lanes per token; with few tokens the heads are shared out
+  // to more groups (each forms its token's angles again) until about eight
+  // CTAs per SM have work
+  fqa_status st = FQA_OK;
+  if (!status_ptr(&st)) return st;
+  const int64_t blocks = ((int64_t)B * N + 15) / 16;
+  int64_t chunks = std::min<int64_t>(total, std::max<int64_t>(1, 8LL * num_sms() / blocks));
+  p.heads_per_group = (int)((total + chunks - 1) / chunks);
+  const dim3 grid((unsigned)blocks, (unsigned)((total + p.heads_per_group - 1) / p.heads_per_group));
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  using Fn = void (*)(const RotaryParams);
+  const Fn fns[3][2] = {{rotary_kernel<__nv_bfloat16, false>, rotary_kernel<__nv_bfloat16, true>},
+                        {rotary_kernel<float, false>, rotary_kernel<float, true>},
+                        {rotary_kernel<__half, false>, rotary_kernel<__half, true>}};
+  fns[dtype][split]<<<grid, 256, 0, s>>>(p);
   return launch_status();
 }
 

@@ -1,0 +1,449 @@
+// microscale.cuh -- microscaled 8- and 4-bit rows: quantization, the RMS norm
+// that quantizes its output, and the way back.
+//
+// A row of K values is padded with zeros to Kp = 32 ceil(K / 32) and held as
+//   mxfp8  E4M3 elements, one E8M0 scale (a power of two) per 32
+//   mxfp4  E2M1 elements, one E8M0 scale per 32
+//   nvfp4  E2M1 elements, one E4M3 scale per 16, one binary32 scale per row
+// Rules (amax over the block, everything round to nearest even, saturating):
+//   mx:    2^e the smallest power of two (e >= -127) with amax <= L 2^e,
+//          L = 448 (E4M3) or 6 (E2M1): no element saturates;
+//          code = RN(x 2^-e), an exact product but for subnormal results
+//   nvfp4: the row's 2^e the smallest power of two (e >= -126) with
+//          amax_row <= 2688 2^e (2688 = 6 * 448, so no block scale
+//          saturates); s = E4M3(fl32(amax 2^-e / 6)); code = E2M1(x 2^-e / s),
+//          0 where s is 0.  A power of two keeps x 2^-e and every tie of 16-bit
+//          inputs exact, so the codes are those of exact arithmetic.
+// The quotient by s is x hi + x lo with hi = 1 / s in binary32 and lo the rest
+// of 1 / s: one multiply and one FMA instead of a division per element, right on
+// every tie (a tie is a product of s with a multiple of 1/4).
+// Non-finite values: an mx block that holds one gets the scale 0xFF (NaN) and
+// zero codes, an nvfp4 row gets a NaN row scale, zero scales and codes.
+//
+// Scales are kept in the order the block-scaled MMA wants them in tensor
+// memory: tiles of 128 rows x 4 blocks, 512 bytes, [row / 128][block / 4]
+// [row % 32][row / 32 % 4][block % 4].  A row's four scales of a tile are one
+// aligned word; the words of a row are written whole, blocks past Kp as 0.
+#pragma once
+
+#include "device.cuh"
+
+namespace fqa {
+
+enum MxFormat : int { kMxFp8 = 0, kMxFp4 = 1, kNvFp4 = 2 };
+
+template <int FMT>
+struct MxTraits {
+  static constexpr int kBlock = FMT == kNvFp4 ? 16 : 32;     // elements per scale
+  static constexpr int kBlockChunks = kBlock / 8;            // threads (8 elements each) per scale
+  static constexpr int kWordChunks = 4 * kBlockChunks;       // threads per word of four scales
+};
+
+__host__ __device__ constexpr int mx_block(int fmt) { return fmt == kNvFp4 ? 16 : 32; }
+__host__ __device__ constexpr int mx_per_byte(int fmt) { return fmt == kMxFp8 ? 1 : 2; }
+
+// ------------------------------------------------------- element access
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two binary32 values -> one word of two 16-bit values, `lo` first in memory.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// W consecutive elements (W * sizeof(T) a multiple of 8 bytes) as binary32;
+// the address is aligned to min(16, W * sizeof(T)) bytes.
+template <typename T, int W>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[W]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const float4 f = reinterpret_cast<const float4*>(p)[i];
+      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+    }
+  } else {
+    uint32_t w[W / 2];
+    if constexpr (W == 8) {
+      const uint4 r = *reinterpret_cast<const uint4*>(p);
+      w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+    } else {
+      static_assert(W == 4, "four or eight elements");
+      const uint2 r = *reinterpret_cast<const uint2*>(p);
+      w[0] = r.x; w[1] = r.y;
+    }
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      const float2 f = unpack2<T>(w[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+template <typename T, int W>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[W]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else if constexpr (W == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
+                                              pack2<T>(v[6], v[7]));
+  } else {
+    static_assert(W == 4, "four or eight elements");
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+  }
+}
+
+// Elements [c0, c0 + 8) of a row of K (zeros past K); `vec`: the row's start
+// is 16-byte aligned and K a multiple of 8, so a chunk is whole or absent.
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T* row, int c0, int K, bool vec, float (&v)[8]) {
+  if (vec && c0 < K) {
+    load_vec<T, 8>(row + c0, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e < K ? to_f32<T>(row[c0 + e]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* row, int c0, int K, bool vec, const float (&v)[8]) {
+  if (vec && c0 < K) {
+    store_vec<T, 8>(row + c0, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c0 + e < K) row[c0 + e] = from_f32<T>(v[e]);
+  }
+}
+
+// ----------------------------------------------------------- the codes
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Largest |v| of eight values as its bit pattern: ordered like the magnitude,
+// and at or above 0x7F800000 exactly when one of them is not finite.
+__device__ __forceinline__ uint32_t chunk_amax(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, abs_bits(v[e]));
+  return m;
+}
+
+// Exponent byte of the smallest power of two whose `largest` multiple
+// reaches the magnitude, largest = 2^top (1 + part / 2^23); not below `low`.
+__device__ __forceinline__ int power_byte(uint32_t amax, int top, uint32_t part, int low) {
+  const int b = (int)(amax >> 23) - top + ((amax & 0x7FFFFFu) > part ? 1 : 0);
+  return b < low ? low : b;
+}
+
+// 2^(127 - byte) for 0 <= byte <= 253.
+__device__ __forceinline__ float inverse_power(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
+
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  return e2m1x2(v[0], v[1]) | (e2m1x2(v[2], v[3]) << 8) | (e2m1x2(v[4], v[5]) << 16) | (e2m1x2(v[6], v[7]) << 24);
+}
+
+struct MxRowParams {
+  const void* x;          // [M] rows of K, row stride ldx (elements)
+  const void* residual;   // the same shape, row stride ldr; binary32 if res_f32, else x's type
+  void* residual_out;     // contiguous [M,K], residual's type
+  const void* weight;     // [K], binary32 if w_f32, else x's type
+  int64_t ldx, ldr;
+  float eps;
+  int M, K, Kp, KT;       // KT words of four scales per row
+  int res_f32, w_f32;
+  int vec_x, vec_r, vec_o, vec_w;
+  uint8_t* codes;         // [M, Kp] or [M, Kp / 2]
+  uint32_t* scales;       // tiles, as words
+  float* row_scale;       // [M] (nvfp4)
+};
+
+// Writes chunk c (elements [8c, 8c + 8)) of a row.  Called by whole warps with
+// consecutive c, so the threads of a scale and of a word are neighbours.
+// row_amax: the row's largest magnitude (nvfp4).
+template <int FMT>
+__device__ __forceinline__ void emit_chunk(const MxRowParams& p, int row, int c, const float (&v)[8], uint32_t row_amax) {
+  using F = MxTraits<FMT>;
+  uint32_t amax = chunk_amax(v);
+#pragma unroll
+  for (int o = 1; o < F::kBlockChunks; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  uint32_t byte;
+  float q[8];
+  if constexpr (FMT == kNvFp4) {
+    byte = 0;
+    float hi = 0.0f, lo = 0.0f, inv = 0.0f;
+    if (row_amax < 0x7F800000u) {
+      inv = inverse_power(power_byte(row_amax, 11, 0x280000u, 1));
+      byte = e4m3x2(__fdiv_rn(__uint_as_float(amax) * inv, 6.0f), 0.0f) & 0xFFu;
+      if (byte != 0) {
+        const float s = e4m3x2_to_f2(byte).x;
+        hi = __frcp_rz(s);             // rounded down: lo >= 0, so a zero keeps its sign below
+        lo = __fmul_rn(__fmaf_rn(-s, hi, 1.0f), hi);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = byte != 0 ? __fmul_rn(v[e], inv) : 0.0f;
+      q[e] = __fmaf_rn(y, hi, __fmul_rn(y, lo));
+    }
+  } else {
+    const bool finite = amax < 0x7F800000u;
+    byte = finite ? (uint32_t)(FMT == kMxFp8 ? power_byte(amax, 8, 0x600000u, 0) : power_byte(amax, 2, 0x400000u, 0))
+                  : 0xFFu;
+    const float inv = inverse_power(finite ? (int)byte : 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = finite ? __fmul_rn(v[e], inv) : 0.0f;
+  }
+  if (8 * c < p.Kp) {
+    if constexpr (FMT == kMxFp8)
+      *reinterpret_cast<uint2*>(p.codes + (size_t)row * p.Kp + 8 * (size_t)c) =
+          make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+    else
+      *reinterpret_cast<uint32_t*>(p.codes + (size_t)row * (p.Kp / 2) + 4 * (size_t)c) = e2m1x8(q);
+  }
+  // the word of four scales: each scale's threads shift theirs into place
+  uint32_t w = byte << (8 * ((c / F::kBlockChunks) & 3));
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, F::kBlockChunks);
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * F::kBlockChunks);
+  const int word = c / F::kWordChunks;
+  if (c % F::kWordChunks == 0 && word < p.KT)
+    p.scales[((size_t)(row >> 7) * p.KT + word) * 128 + (row & 31) * 4 + ((row >> 5) & 3)] = w;
+}
+
+// Reductions over the TPR threads of a row (one warp, or the whole CTA).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = lane < TPR / 32 ? red[lane] : 0.0f;
+#pragma unroll
+    for (int o = TPR / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = __shfl_sync(0xFFFFFFFFu, v, 0);
+  }
+  return v;
+}
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xFFFFFFFFu, v);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = __reduce_max_sync(0xFFFFFFFFu, lane < TPR / 32 ? red[lane] : 0u);
+  }
+  return v;
+}
+
+// One row per TPR threads, NCH chunks of 8 elements each held in registers
+// (kLoop: rows longer than TPR * NCH * 8 are read again for each step
+// instead).  Normed: h = x + residual in binary32, residual_out = h rounded,
+// y = h / sqrt(mean h^2 + eps) * weight, and y is quantized (never h, so the
+// norm sees the sum before its rounding).
+template <typename T, int FMT, bool kNorm, int TPR, int NCH, bool kLoop>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxRowParams p) {
+  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+  __shared__ float red_sum[TPR / 32];
+  __shared__ uint32_t red_max[TPR / 32];
+  const int t = threadIdx.x % TPR;
+  const int row = blockIdx.x * kRows + threadIdx.x / TPR;
+  if (row >= p.M) return;                       // whole warps (and, for TPR >= 128, no CTA)
+  const T* x = static_cast<const T*>(p.x) + (int64_t)row * p.ldx;
+  const bool res = kNorm && p.residual != nullptr;
+
+  auto load_h = [&](int c, float (&v)[8]) {
+    load_chunk<T>(x, 8 * c, p.K, p.vec_x, v);
+    if (res) {
+      float r[8];
+      if (p.res_f32)
+        load_chunk<float>(static_cast<const float*>(p.residual) + (int64_t)row * p.ldr, 8 * c, p.K, p.vec_r, r);
+      else
+        load_chunk<T>(static_cast<const T*>(p.residual) + (int64_t)row * p.ldr, 8 * c, p.K, p.vec_r, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += r[e];
+    }
+  };
+  auto store_h = [&](int c, const float (&v)[8]) {
+    if (p.res_f32)
+      store_chunk<float>(static_cast<float*>(p.residual_out) + (int64_t)row * p.K, 8 * c, p.K, p.vec_o, v);
+    else
+      store_chunk<T>(static_cast<T*>(p.residual_out) + (int64_t)row * p.K, 8 * c, p.K, p.vec_o, v);
+  };
+  auto normed = [&](int c, float rstd, float (&v)[8]) {
+    float w[8];
+    if (p.w_f32)
+      load_chunk<float>(static_cast<const float*>(p.weight), 8 * c, p.K, p.vec_w, w);
+    else
+      load_chunk<T>(static_cast<const T*>(p.weight), 8 * c, p.K, p.vec_w, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 8 * c + e < p.K ? v[e] * rstd * w[e] : 0.0f;   // (no 0 * inf past K)
+  };
+
+  if constexpr (!kLoop) {
+    float v[NCH][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) load_h(t + j * TPR, v[j]);
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += v[j][e] * v[j][e];
+      if (res) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) store_h(t + j * TPR, v[j]);
+      }
+      const float rstd = rsqrtf(__fdiv_rn(row_sum<TPR>(ss, red_sum), (float)p.K) + p.eps);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) normed(t + j * TPR, rstd, v[j]);
+    }
+    uint32_t amax = 0;
+    if constexpr (FMT == kNvFp4) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) amax = max(amax, chunk_amax(v[j]));
+      amax = row_max<TPR>(amax, red_max);
+    }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) emit_chunk<FMT>(p, row, t + j * TPR, v[j], amax);
+    if (FMT == kNvFp4 && t == 0)
+      p.row_scale[row] = amax < 0x7F800000u ? __uint_as_float((uint32_t)power_byte(amax, 11, 0x280000u, 1) << 23)
+                                            : __uint_as_float(0x7FC00000u);
+  } else {
+    // a whole number of passes for every thread: the shuffles need full warps
+    const int passes = (p.KT * MxTraits<FMT>::kWordChunks + TPR - 1) / TPR;
+    float rstd = 1.0f;
+    if constexpr (kNorm) {
+      float ss = 0.0f;
+      for (int i = 0; i < passes; ++i) {
+        float v[8];
+        load_h(t + i * TPR, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+      }
+      rstd = rsqrtf(__fdiv_rn(row_sum<TPR>(ss, red_sum), (float)p.K) + p.eps);
+    }
+    uint32_t amax = 0;
+    if constexpr (FMT == kNvFp4) {
+      for (int i = 0; i < passes; ++i) {
+        float v[8];
+        load_h(t + i * TPR, v);
+        if constexpr (kNorm) normed(t + i * TPR, rstd, v);
+        amax = max(amax, chunk_amax(v));
+      }
+      amax = row_max<TPR>(amax, red_max);
+    }
+    // residual_out may be residual itself: each thread writes an element only
+    // here, after its own last read of it
+    for (int i = 0; i < passes; ++i) {
+      float v[8];
+      load_h(t + i * TPR, v);
+      if (res) store_h(t + i * TPR, v);
+      if constexpr (kNorm) normed(t + i * TPR, rstd, v);
+      emit_chunk<FMT>(p, row, t + i * TPR, v, amax);
+    }
+    if (FMT == kNvFp4 && t == 0)
+      p.row_scale[row] = amax < 0x7F800000u ? __uint_as_float((uint32_t)power_byte(amax, 11, 0x280000u, 1) << 23)
+                                            : __uint_as_float(0x7FC00000u);
+  }
+}
+
+// ------------------------------------------------------------ and back
+
+// Two E2M1 codes (bits [0,4) and [4,8)) -> their values.
+__device__ __forceinline__ float2 e2m1x2_to_f2(uint32_t codes) {
+  uint32_t h2;
+  asm("{\n\t.reg .b8 c;\n\tcvt.u8.u32 c, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(h2) : "r"(codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
+}
+
+// E8M0 byte -> 2^(byte - 127); 0 -> 2^-127 (subnormal), 255 -> NaN.
+__device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7FC00000u : (b == 0u ? 0x00400000u : b << 23));
+}
+
+struct MxDequantParams {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* row_scale;
+  void* out;              // contiguous [M, K]
+  int M, K, Kp, KT;
+  int vec;                // K a multiple of 8: whole chunks, 16-byte aligned
+};
+
+// value = element * scale (exact in binary32) * row scale, rounded once more to
+// the output's type.  One thread per chunk of 8 elements.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParams p) {
+  constexpr int kBlock = MxTraits<FMT>::kBlock;
+  const int chunks = (p.K + 7) / 8;
+  const int64_t total = (int64_t)p.M * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int row = (int)(i / chunks), c = (int)(i - (int64_t)row * chunks);
+    const int blk = 8 * c / kBlock;
+    const uint32_t sb = p.scales[((size_t)(row >> 7) * p.KT + (blk >> 2)) * 512 + (row & 31) * 16 +
+                                 ((row >> 5) & 3) * 4 + (blk & 3)];
+    float v[8];
+    if constexpr (FMT == kMxFp8) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p.codes + (size_t)row * p.Kp + 8 * (size_t)c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = e4m3x2_to_f2(((e < 2 ? w.x : w.y) >> (16 * (e & 1))) & 0xFFFFu);
+        v[2 * e] = f.x;
+        v[2 * e + 1] = f.y;
+      }
+    } else {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(p.codes + (size_t)row * (p.Kp / 2) + 4 * (size_t)c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = e2m1x2_to_f2((w >> (8 * e)) & 0xFFu);
+        v[2 * e] = f.x;
+        v[2 * e + 1] = f.y;
+      }
+    }
+    const float s = FMT == kNvFp4 ? e4m3x2_to_f2(sb).x : e8m0_to_f32(sb);
+    const float rs = FMT == kNvFp4 ? __ldg(p.row_scale + row) : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = FMT == kNvFp4 ? v[e] * s * rs : v[e] * s;
+    store_chunk<T>(static_cast<T*>(p.out) + (int64_t)row * p.K, 8 * c, p.K, p.vec, v);
+  }
+}
+
+}  // namespace fqa
