@@ -133,6 +133,40 @@ static bool make_tmap_rows(CUtensorMap* m, const void* base, int row_bytes, int 
   return r == CUDA_SUCCESS;
 }
 
+// 3-D view (word, word column, block of 128 rows) of scale tiles as 32-bit
+// words: a tile is 128 words; box = `words` tiles of `blocks` row blocks.  Tiles
+// past the end read as zeros.
+static bool make_tmap_scales(CUtensorMap* m, const void* base, int KT, int rows, int words, int blocks) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {128, (cuuint64_t)KT, (cuuint64_t)(rows + 127) / 128};
+  cuuint64_t strides[2] = {512ull, 512ull * (cuuint64_t)KT};
+  cuuint32_t box[3] = {128u, (cuuint32_t)words, (cuuint32_t)blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// 2-D view of a product [M, N] for stores of 32 rows x 128 bytes, 128-byte
+// swizzle; rows on 16-byte boundaries.
+static bool make_tmap_out(CUtensorMap* m, const void* base, int type, int M, int N) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return false;
+  const uint32_t elt = type == FQA_DTYPE_F32 ? 4 : 2;
+  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+  cuuint64_t strides[1] = {(cuuint64_t)N * elt};
+  cuuint32_t box[2] = {128u / elt, 32u};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType t = type == FQA_DTYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : type == FQA_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUresult r = enc(m, t, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Shape checks shared by every call: any N >= 1 (the last 64-token block and
@@ -207,6 +241,8 @@ static fqa_status launch_attention_fp8(const void* q, const void* k, const void*
   fn<<<grid, kF8Threads, F8Traits::kSmemBytes, stream>>>(tq, tk, tv, prm);
   return launch_status();
 }
+
+static size_t dtype_bytes(int t) { return t == FQA_DTYPE_F32 ? 4 : 2; }
 
 // -------------------------------------------- launches of microscaled rows
 
@@ -291,12 +327,45 @@ static fqa_status launch_mx_small(const uint8_t* a, const uint8_t* b, const MxMa
 }
 
 template <int FMT>
+static fqa_status launch_mx_large(const uint8_t* a, const uint8_t* b, const MxMatmulParams& p, int row_bytes,
+                                  cudaStream_t s) {
+  using T = MxLarge<FMT>;
+  CUtensorMap ta, tb, tsa, tsb, to{};
+  const int64_t tiles = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256);
+  // rows on 16-byte boundaries leave as TMA stores
+  const size_t elt = dtype_bytes(p.out_type);
+  const bool tma_out = aligned(p.out, 16) && (size_t)p.N * elt % 16 == 0;
+  if (!make_tmap_rows(&ta, a, row_bytes, p.M, 128) || !make_tmap_rows(&tb, b, row_bytes, p.N, 128) ||
+      !make_tmap_scales(&tsa, p.sa, p.KT, p.M, MxMma<FMT>::kWords, 1) ||
+      !make_tmap_scales(&tsb, p.sb, p.KT, p.N, MxMma<FMT>::kWords, 2) ||
+      (tma_out && !make_tmap_out(&to, p.out, p.out_type, p.M, p.N)))
+    return FQA_ERR_CUDA;
+  const auto fn = mx_matmul_large_kernel<FMT>;
+  if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess)
+    return FQA_ERR_CUDA;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(tiles, num_sms() / 2));
+  cfg.blockDim = dim3(kMxLargeThreads);
+  cfg.dynamicSmemBytes = T::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, ta, tb, tsa, tsb, to, p, (int)tma_out) != cudaSuccess) return FQA_ERR_CUDA;
+  return launch_status();
+}
+
+template <int FMT>
 static fqa_status launch_mx_matmul(const uint8_t* a, const uint8_t* b, const MxMatmulParams& p, int row_bytes,
                                    cudaStream_t s) {
   if (p.M <= 16) return launch_mx_small<FMT, 16>(a, b, p, row_bytes, s);
   if (p.M <= 32) return launch_mx_small<FMT, 32>(a, b, p, row_bytes, s);
   if (p.M <= 64) return launch_mx_small<FMT, 64>(a, b, p, row_bytes, s);
-  return launch_mx_small<FMT, 128>(a, b, p, row_bytes, s);
+  if (p.M <= 128) return launch_mx_small<FMT, 128>(a, b, p, row_bytes, s);
+  return launch_mx_large<FMT>(a, b, p, row_bytes, s);
 }
 
 }  // namespace fqa
@@ -690,7 +759,6 @@ fqa_status fqa_attention_nvfp4(const uint8_t* q4, const uint8_t* k4, const uint8
 static bool mx_shape_ok(int64_t rows, int K) { return rows >= 0 && rows <= kMxMaxRows && K >= 1 && K <= kMxMaxCols; }
 static bool mx_format_ok(int fmt) { return fmt == FQA_MXFP8 || fmt == FQA_MXFP4 || fmt == FQA_NVFP4; }
 static bool dtype_ok(int t) { return t == FQA_DTYPE_BF16 || t == FQA_DTYPE_F32 || t == FQA_DTYPE_F16; }
-static size_t dtype_bytes(int t) { return t == FQA_DTYPE_F32 ? 4 : 2; }
 static int mx_padded(int K) { return (K + 31) / 32 * 32; }
 static int mx_words(int K, int fmt) { return (mx_padded(K) + 4 * mx_block(fmt) - 1) / (4 * mx_block(fmt)); }
 

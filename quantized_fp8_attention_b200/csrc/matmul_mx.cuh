@@ -284,4 +284,383 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   }
 }
 
+// ------------------------------------------------------ many rows of A
+//
+// 256 x 256 tiles by pairs of CTAs (cta_group::2): each CTA holds 128 rows of
+// A and 128 of B per stage, the pair's tensor cores share both, so a stage of
+// 256 4-bit channels costs each SM 32 KB of codes for 512 cycles of MMAs: the
+// largest tile tensor memory allows and the one with the least traffic per
+// product.  Persistent: a pair walks over its tiles, and the producer runs
+// ahead into the next tile while the epilogue drains the last.
+//   warp 0     TMA producer (both CTAs; completion on the leader's barriers)
+//   warp 1     TMEM owner; in the leader CTA also the MMA issuer
+//   warps 4-11 epilogue: lane quarter warp % 4, columns 128 (warp / 4 - 1) ..
+// Tensor memory: the tile's 256 columns of sums, then per stage 4 columns per
+// word for A's scales and 8 for B's (both CTAs need all of B's).  There is no
+// room for a second tile of sums, so the epilogue first moves its 128 columns
+// into registers and gives the columns back before it scales, rounds and
+// stores.  Stores go through shared memory, 32 rows x 128 bytes a warp and
+// step, as TMA stores (or, where the output's rows are not on 16-byte
+// boundaries, as coalesced element stores).
+constexpr int kMxLargeThreads = 384;
+
+template <int FMT>
+struct MxLarge {
+  using Mma = MxMma<FMT>;
+  static constexpr int kOpBytes = 128 * 128;
+  static constexpr int kSfaBytes = 512 * Mma::kWords, kSfbBytes = 1024 * Mma::kWords;
+  static constexpr int kStageBytes = (2 * kOpBytes + kSfaBytes + kSfbBytes + 1023) / 1024 * 1024;
+  static constexpr int kTxBytes = 2 * (2 * kOpBytes + kSfaBytes + kSfbBytes);   // both CTAs
+  static constexpr int kStages = 5;
+  static constexpr int kOffStage = 0;
+  static constexpr int kOffOut = kStages * kStageBytes;      // 8 warps x 4 KB
+  static constexpr int kOffCol = kOffOut + 8 * 4096;         // row scales and bias of the tile's columns
+  static constexpr int kOffBar = kOffCol + 2 * 256 * 4;
+  static constexpr int kSmemBytes = kOffBar + (2 * kStages + 2) * 8 + 16 + 1024;
+  static constexpr int kColSf = 256, kSfCols = 12 * Mma::kWords;
+  static_assert(kColSf + kStages * kSfCols <= 512, "tensor memory");
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+// Shared address of the same offset in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait() for a barrier that the other CTA arrives on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                  uint32_t* status) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+// Tiled loads of a CTA pair: the destination is this CTA's, the barrier may
+// be the peer's (both given as shared addresses of the cluster).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x,
+                                                 int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// 2-D tiled store; x on a 16-byte boundary and not negative.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// tc_commit() of a pair: arrives on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Tile t of mt x nt: bands of eight row tiles, column by column within a
+// band, so that the pairs at work share A's and B's tiles in L2.
+__device__ __forceinline__ void large_tile(int64_t t, int mt, int nt, int& m, int& n) {
+  const int64_t band = t / (8LL * nt);
+  const int rows = min(8, mt - (int)band * 8);
+  const int in = (int)(t - band * 8LL * nt);
+  n = in / rows;
+  m = (int)band * 8 + in % rows;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kMxLargeThreads, 1)
+    mx_matmul_large_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
+                           const __grid_constant__ CUtensorMap tmOut, const MxMatmulParams p, int tma_out) {
+  using T = MxLarge<FMT>;
+  using Mma = MxMma<FMT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::kOffBar);
+  uint64_t* empty = full + T::kStages;
+  uint64_t* acc_full = empty + T::kStages;
+  uint64_t* acc_free = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x & 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int mt = (p.M + 255) / 256, nt = (p.N + 255) / 256;
+  const int64_t tiles = (int64_t)mt * nt;
+  const int stages = (p.mmas + 3) / 4;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) {
+      mbar_init(&full[s], 1);        // the leader's expectation; bytes from both CTAs
+      mbar_init(&empty[s], 1);       // the pair's commit
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 16);         // the epilogue warps of both CTAs
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();                // the peer's barriers are ready too
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer
+    if (lane == 0) {
+      int i = 0;                     // stages issued so far
+      bool ok = true;
+      for (int64_t t = pair; ok && t < tiles; t += pairs) {
+        int mi, ni;
+        large_tile(t, mt, nt, mi, ni);
+        const int arow = mi * 256 + 128 * (int)rank, brow = ni * 256 + 128 * (int)rank;
+        for (int s = 0; s < stages; ++s, ++i) {
+          const int slot = i % T::kStages;
+          if (!(ok = mbar_wait_cluster(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status))) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[slot], T::kTxBytes);
+          const uint32_t bar = mapa_u32(smem_u32(&full[slot]), 0);
+          const uint32_t st = mapa_u32(smem_u32(smem + slot * T::kStageBytes), rank);
+          tma_load_2d_pair(st, &tmA, bar, s * 128, arow);
+          tma_load_2d_pair(st + T::kOpBytes, &tmB, bar, s * 128, brow);
+          tma_load_3d_pair(st + 2 * T::kOpBytes, &tmSa, bar, 0, s * Mma::kWords, arow / 128);
+          tma_load_3d_pair(st + 2 * T::kOpBytes + T::kSfaBytes, &tmSb, bar, 0, s * Mma::kWords, ni * 2);
+        }
+      }
+      // nothing may reach this CTA after it ends: the slots' last releases, or
+      // after a timeout the copies in flight (which complete on the leader's
+      // barriers: long done after two milliseconds)
+      if (ok)
+        for (int j = i > T::kStages ? i - T::kStages : 0; j < i; ++j)
+          if (!mbar_wait_cluster(&empty[j % T::kStages], (j / T::kStages) & 1, abort_flag, p.status)) break;
+      if (*abort_flag)
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kI = Mma::idesc(256, 256);
+      int i = 0, done = 0;
+      bool ok = true;
+      for (int64_t t = pair; ok && t < tiles; t += pairs, ++done) {
+        // the last tile's sums have left tensor memory
+        if (!(ok = mbar_wait_cluster(acc_free, (done & 1) ^ 1, abort_flag, p.status))) break;
+        tc_fence_after();
+        for (int s = 0; s < stages; ++s, ++i) {
+          const int slot = i % T::kStages;
+          if (!(ok = mbar_wait_cluster(&full[slot], (i / T::kStages) & 1, abort_flag, p.status))) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
+          const uint32_t sf = st + 2 * T::kOpBytes;
+          const uint32_t tsa = tmem + T::kColSf + slot * T::kSfCols, tsb = tsa + 4 * Mma::kWords;
+          // B's two blocks of 128 rows land word by word side by side: eight
+          // columns per word
+#pragma unroll
+          for (int w = 0; w < (int)Mma::kWords; ++w) {
+            tmem_cp_scales<2>(tsa + 4 * w, make_sdesc_plain(sf + 512 * w));
+            tmem_cp_scales<2>(tsb + 8 * w, make_sdesc_plain(sf + T::kSfaBytes + 512 * w));
+            tmem_cp_scales<2>(tsb + 8 * w + 4, make_sdesc_plain(sf + T::kSfaBytes + 512 * (Mma::kWords + w)));
+          }
+          const uint64_t dA = make_sdesc_sw128(st, 16, 1024), dB = make_sdesc_sw128(st + T::kOpBytes, 16, 1024);
+          const int left = p.mmas - 4 * s;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk >= left) break;
+            const uint32_t ids = (Mma::sf_id(kk) << 4) | (Mma::sf_id(kk) << 29);
+            mma_mx<FMT, 2>(tmem, dA + 2 * kk, dB + 2 * kk, kI | ids, tsa + 4 * Mma::word(kk),
+                           tsb + 8 * Mma::word(kk), s > 0 || kk > 0);
+          }
+          tc_commit_pair(&empty[slot]);
+        }
+        if (ok) tc_commit_pair(acc_full);
+      }
+      if (!ok) {                     // MMAs in flight end before the CTA does
+        tc_commit_pair(acc_full);
+        mbar_wait_drain(acc_full, done & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp >> 2) - 1;
+    const int et = threadIdx.x - 128;                         // 0..255
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128u * (uint32_t)half;
+    const uint32_t stage = smem_u32(smem + T::kOffOut + (warp - 4) * 4096);
+    const uint32_t free_leader = mapa_u32(smem_u32(acc_free), 0);
+    const bool cols = p.rb != nullptr || p.bias != nullptr;
+    int done = 0;
+    bool ok = true;                  // after a timeout the warps still meet at the barriers below
+    for (int64_t t = pair; t < tiles; t += pairs, ++done) {
+      int mi, ni;
+      large_tile(t, mt, nt, mi, ni);
+      const int row0 = mi * 256 + 128 * (int)rank + 32 * q, n0 = ni * 256 + 128 * half;
+      float* sc = reinterpret_cast<float*>(smem + T::kOffCol);
+      if (cols) {
+        bar_sync(1, 256);            // everyone is through with the last tile's
+        const int n = ni * 256 + et;
+        sc[et] = (p.rb != nullptr && n < p.N) ? __ldg(p.rb + n) : 1.0f;
+        sc[256 + et] = (p.bias != nullptr && n < p.N) ? __ldg(p.bias + n) : 0.0f;
+        bar_sync(1, 256);
+      }
+      const float ra = (p.ra != nullptr && row0 + lane < p.M) ? __ldg(p.ra + row0 + lane) : 1.0f;
+      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_full, done & 1, abort_flag, p.status));
+      if (!ok) continue;
+      tc_fence_after();
+      uint32_t u[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(acc + 32u * c, u[c]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(free_leader);
+      const float* rb = sc + 128 * half;
+      const float* bias = rb + 256;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (cols) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(rb + 32 * c + e);
+            const float4 g = *reinterpret_cast<const float4*>(bias + 32 * c + e);
+            u[c][e] = __float_as_uint(fmaf(__uint_as_float(u[c][e]) * ra, f.x, g.x));
+            u[c][e + 1] = __float_as_uint(fmaf(__uint_as_float(u[c][e + 1]) * ra, f.y, g.y));
+            u[c][e + 2] = __float_as_uint(fmaf(__uint_as_float(u[c][e + 2]) * ra, f.z, g.z));
+            u[c][e + 3] = __float_as_uint(fmaf(__uint_as_float(u[c][e + 3]) * ra, f.w, g.w));
+          }
+        }
+      }
+      if (row0 >= p.M) continue;
+      // one step: 32 rows x 128 bytes (64 16-bit or 32 binary32 columns)
+      const uint32_t line = stage + (uint32_t)lane * 128u, sw = (uint32_t)(lane & 7);
+      auto flush = [&](int col0, int width) {
+        if (tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && n0 + col0 < p.N) {
+            tma_store_2d(&tmOut, stage, n0 + col0, row0);
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          const int rows = min(32, p.M - row0);
+          for (int r = 0; r < rows; ++r) {
+            for (int j = lane; j < width; j += 32) {
+              const int n = n0 + col0 + j;
+              if (n >= p.N) continue;
+              const size_t at = (size_t)(row0 + r) * p.N + n;
+              const uint32_t b = (uint32_t)j * (128u / (uint32_t)width);
+              const uint32_t addr = stage + (uint32_t)r * 128u + (((b >> 4) ^ (uint32_t)(r & 7)) << 4) + (b & 15u);
+              if (width == 32) {
+                uint32_t v;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+                static_cast<uint32_t*>(p.out)[at] = v;
+              } else {
+                uint16_t v;
+                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr));
+                static_cast<uint16_t*>(p.out)[at] = v;
+              }
+            }
+          }
+          __syncwarp();
+        }
+      };
+      auto ready = [&]() {           // the last step's store has read the buffer
+        if (tma_out && lane == 0) bulk_wait_read();
+        __syncwarp();
+      };
+      if (p.out_type == 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          ready();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4(line + (((uint32_t)j ^ sw) << 4), u[c][4 * j], u[c][4 * j + 1], u[c][4 * j + 2],
+                         u[c][4 * j + 3]);
+          flush(32 * c, 32);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          ready();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float lo = __uint_as_float(u[2 * c + j / 4][8 * (j % 4) + 2 * e]);
+              const float hi = __uint_as_float(u[2 * c + j / 4][8 * (j % 4) + 2 * e + 1]);
+              w[e] = p.out_type == 0 ? pack2<__nv_bfloat16>(lo, hi) : pack2<__half>(lo, hi);
+            }
+            st_shared_v4(line + (((uint32_t)j ^ sw) << 4), w[0], w[1], w[2], w[3]);
+          }
+          flush(64 * c, 64);
+        }
+      }
+    }
+    if (tma_out && lane == 0) bulk_wait_read();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
 }  // namespace fqa
