@@ -173,14 +173,16 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // (both issuing warps stay whole and elect a lane per step: see the issuer of
+  // the large kernel)
   if (warp == 0) {
-    if (lane == 0) {
-      int issued = 0;
-      for (int s = s0; s < s1; ++s) {
-        const int i = s - s0, slot = i % T::kStages;
-        if (!mbar_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status)) break;
+    int issued = 0;
+    for (int s = s0; s < s1; ++s) {
+      const int i = s - s0, slot = i % T::kStages;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status))) break;
+      if (elect_one()) {
         uint8_t* st = smem + slot * T::kStageBytes;
-        const uint32_t words = min(Mma::kWords, p.KT - s * Mma::kWords);
+        const uint32_t words = min((int)Mma::kWords, p.KT - s * (int)Mma::kWords);
         mbar_arrive_expect_tx(&full[slot], T::kPBytes + T::kQBytes + 2 * 512 * words);
         tma_load_2d(st, &tmP, &full[slot], s * 128, p0);
         tma_load_2d(st + T::kPBytes, &tmQ, &full[slot], s * 128, q0);
@@ -188,47 +190,50 @@ __global__ void __launch_bounds__(kMxSmallThreads)
         const size_t w0 = (size_t)s * Mma::kWords * 512;
         bulk_load_plain(sf, p.sb + (size_t)(p0 / 128) * p.KT * 512 + w0, 512 * words, &full[slot]);
         bulk_load_plain(sf + T::kSfBytes, p.sa + (size_t)(q0 / 128) * p.KT * 512 + w0, 512 * words, &full[slot]);
-        issued = i + 1;
       }
-      if (*abort_flag)      // no copy may be in flight when the CTA ends
-        for (int i = issued > T::kStages ? issued - T::kStages : 0; i < issued; ++i)
-          mbar_wait_drain(&full[i % T::kStages], (i / T::kStages) & 1);
+      __syncwarp();
+      issued = i + 1;
     }
+    if (*abort_flag)        // no copy may be in flight when the CTA ends
+      for (int i = issued > T::kStages ? issued - T::kStages : 0; i < issued; ++i)
+        mbar_wait_drain(&full[i % T::kStages], (i / T::kStages) & 1);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t kI = Mma::idesc(128, NT);
-      bool any = false;
-      // the Q tile's place in its block of 128 rows: 32 rows per column (a tile of
-      // 16 rows is only taken where it is the only one, at row 0)
-      const uint32_t qcol = (uint32_t)(q0 % 128) / 32;
-      for (int s = s0; s < s1; ++s) {
-        const int i = s - s0, slot = i % T::kStages;
-        if (!mbar_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status)) break;
-        tc_fence_after();
-        const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
-        const uint32_t sf = st + T::kStageBytes - 2 * T::kSfBytes;
-        const uint32_t tsp = tmem + T::kColSf + slot * T::kSfCols, tsq = tsp + 4 * Mma::kWords;
-        const int words = min(Mma::kWords, p.KT - s * Mma::kWords);
-        for (int w = 0; w < words; ++w) {
-          tmem_cp_scales<1>(tsp + 4 * w, make_sdesc_plain(sf + 512 * w));
-          tmem_cp_scales<1>(tsq + 4 * w, make_sdesc_plain(sf + T::kSfBytes + 512 * w));
+    constexpr uint32_t kI = Mma::idesc(128, NT);
+    // the Q tile's place in its block of 128 rows: 32 rows per column (a tile of
+    // 16 rows is only taken where it is the only one, at row 0)
+    const uint32_t qcol = (uint32_t)(q0 % 128) / 32;
+    for (int s = s0; s < s1; ++s) {
+      const int i = s - s0, slot = i % T::kStages;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status))) break;
+      tc_fence_after();
+      const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
+      const uint32_t sf = st + T::kStageBytes - 2 * T::kSfBytes;
+      const uint32_t tsp = tmem + T::kColSf + slot * T::kSfCols, tsq = tsp + 4 * Mma::kWords;
+      const int words = min((int)Mma::kWords, p.KT - s * (int)Mma::kWords), left = p.mmas - 4 * s;
+      const uint64_t dP = make_sdesc_sw128(st, 16, 1024), dQ = make_sdesc_sw128(st + T::kPBytes, 16, 1024);
+      const uint64_t dSp = make_sdesc_plain(sf), dSq = make_sdesc_plain(sf + T::kSfBytes);
+      if (elect_one()) {
+#pragma unroll
+        for (int w = 0; w < (int)Mma::kWords; ++w) {
+          if (w >= words) break;
+          tmem_cp_scales<1>(tsp + 4 * w, dSp + 32 * w);
+          tmem_cp_scales<1>(tsq + 4 * w, dSq + 32 * w);
         }
-        const uint64_t dP = make_sdesc_sw128(st, 16, 1024), dQ = make_sdesc_sw128(st + T::kPBytes, 16, 1024);
-        const int left = p.mmas - 4 * s;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (kk >= left) break;
           const uint32_t ids = (Mma::sf_id(kk) << 4) | (Mma::sf_id(kk) << 29);
           mma_mx<FMT, 1>(tmem, dP + 2 * kk, dQ + 2 * kk, kI | ids, tsp + 4 * Mma::word(kk),
-                         tsq + 4 * Mma::word(kk) + qcol, any);
-          any = true;
+                         tsq + 4 * Mma::word(kk) + qcol, s > s0 || kk > 0);
         }
         tc_commit(&empty[slot]);
       }
-      tc_commit(done);      // also after a timeout: nothing is in flight when the tile ends
-      mbar_wait_drain(done, 0);
+      __syncwarp();
     }
+    if (elect_one()) tc_commit(done);   // also after a timeout: nothing is in flight when the tile ends
+    __syncwarp();
+    mbar_wait_drain(done, 0);
     __syncwarp();
   }
   // ------------------------------------------------ epilogue
@@ -360,6 +365,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same for a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                  uint32_t* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity, abort_flag, status));
+}
+
 // Tiled loads of a CTA pair: the destination is this CTA's, the barrier may
 // be the peer's (both given as shared addresses of the cluster).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x,
@@ -460,16 +471,16 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ producer
-    if (lane == 0) {
-      int i = 0;                     // stages issued so far
-      bool ok = true;
-      for (int64_t t = pair; ok && t < tiles; t += pairs) {
-        int mi, ni;
-        large_tile(t, mt, nt, mi, ni);
-        const int arow = mi * 256 + 128 * (int)rank, brow = ni * 256 + 128 * (int)rank;
-        for (int s = 0; s < stages; ++s, ++i) {
-          const int slot = i % T::kStages;
-          if (!(ok = mbar_wait_cluster(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status))) break;
+    int i = 0;                       // stages issued so far
+    bool ok = true;
+    for (int64_t t = pair; ok && t < tiles; t += pairs) {
+      int mi, ni;
+      large_tile(t, mt, nt, mi, ni);
+      const int arow = mi * 256 + 128 * (int)rank, brow = ni * 256 + 128 * (int)rank;
+      for (int s = 0; s < stages; ++s, ++i) {
+        const int slot = i % T::kStages;
+        if (!(ok = warp_wait_cluster(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status))) break;
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[slot], T::kTxBytes);
           const uint32_t bar = mapa_u32(smem_u32(&full[slot]), 0);
           const uint32_t st = mapa_u32(smem_u32(smem + slot * T::kStageBytes), rank);
@@ -478,45 +489,51 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
           tma_load_3d_pair(st + 2 * T::kOpBytes, &tmSa, bar, 0, s * Mma::kWords, arow / 128);
           tma_load_3d_pair(st + 2 * T::kOpBytes + T::kSfaBytes, &tmSb, bar, 0, s * Mma::kWords, ni * 2);
         }
+        __syncwarp();
       }
-      // nothing may reach this CTA after it ends: the slots' last releases, or
-      // after a timeout the copies in flight (which complete on the leader's
-      // barriers: long done after two milliseconds)
-      if (ok)
-        for (int j = i > T::kStages ? i - T::kStages : 0; j < i; ++j)
-          if (!mbar_wait_cluster(&empty[j % T::kStages], (j / T::kStages) & 1, abort_flag, p.status)) break;
-      if (*abort_flag)
-        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
-        }
     }
+    // nothing may reach this CTA after it ends: the slots' last releases, or
+    // after a timeout the copies in flight (which complete on the leader's
+    // barriers: long done after two milliseconds)
+    if (ok)
+      for (int j = i > T::kStages ? i - T::kStages : 0; j < i; ++j)
+        if (!warp_wait_cluster(&empty[j % T::kStages], (j / T::kStages) & 1, abort_flag, p.status)) break;
+    if (*abort_flag)
+      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
+      }
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kI = Mma::idesc(256, 256);
-      int i = 0, done = 0;
-      bool ok = true;
-      for (int64_t t = pair; ok && t < tiles; t += pairs, ++done) {
-        // the last tile's sums have left tensor memory
-        if (!(ok = mbar_wait_cluster(acc_free, (done & 1) ^ 1, abort_flag, p.status))) break;
+    // The whole warp walks through the loop and one elected lane issues: the
+    // descriptors then stay in uniform registers.  From a branch of a single
+    // lane each tcgen05 instruction took about 70 cycles to issue (16 of them
+    // per stage: 1086 cycles for 512 cycles of MMAs), so the copies alone
+    // halved the rate.
+    constexpr uint32_t kI = Mma::idesc(256, 256);
+    int i = 0, done = 0;
+    bool ok = true;
+    for (int64_t t = pair; ok && t < tiles; t += pairs, ++done) {
+      // the last tile's sums have left tensor memory
+      if (!(ok = warp_wait_cluster(acc_free, (done & 1) ^ 1, abort_flag, p.status))) break;
+      for (int s = 0; s < stages; ++s, ++i) {
+        const int slot = i % T::kStages;
+        if (!(ok = warp_wait_cluster(&full[slot], (i / T::kStages) & 1, abort_flag, p.status))) break;
         tc_fence_after();
-        for (int s = 0; s < stages; ++s, ++i) {
-          const int slot = i % T::kStages;
-          if (!(ok = mbar_wait_cluster(&full[slot], (i / T::kStages) & 1, abort_flag, p.status))) break;
-          tc_fence_after();
-          const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
-          const uint32_t sf = st + 2 * T::kOpBytes;
-          const uint32_t tsa = tmem + T::kColSf + slot * T::kSfCols, tsb = tsa + 4 * Mma::kWords;
+        const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
+        const uint32_t tsa = tmem + T::kColSf + slot * T::kSfCols, tsb = tsa + 4 * Mma::kWords;
+        const uint64_t dA = make_sdesc_sw128(st, 16, 1024), dB = make_sdesc_sw128(st + T::kOpBytes, 16, 1024);
+        const uint64_t dSa = make_sdesc_plain(st + 2 * T::kOpBytes);
+        const uint64_t dSb = make_sdesc_plain(st + 2 * T::kOpBytes + T::kSfaBytes);
+        const int left = p.mmas - 4 * s;
+        if (elect_one()) {
           // B's two blocks of 128 rows land word by word side by side: eight
           // columns per word
 #pragma unroll
           for (int w = 0; w < (int)Mma::kWords; ++w) {
-            tmem_cp_scales<2>(tsa + 4 * w, make_sdesc_plain(sf + 512 * w));
-            tmem_cp_scales<2>(tsb + 8 * w, make_sdesc_plain(sf + T::kSfaBytes + 512 * w));
-            tmem_cp_scales<2>(tsb + 8 * w + 4, make_sdesc_plain(sf + T::kSfaBytes + 512 * (Mma::kWords + w)));
+            tmem_cp_scales<2>(tsa + 4 * w, dSa + 32 * w);
+            tmem_cp_scales<2>(tsb + 8 * w, dSb + 32 * w);
+            tmem_cp_scales<2>(tsb + 8 * w + 4, dSb + 32 * (Mma::kWords + w));
           }
-          const uint64_t dA = make_sdesc_sw128(st, 16, 1024), dB = make_sdesc_sw128(st + T::kOpBytes, 16, 1024);
-          const int left = p.mmas - 4 * s;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk >= left) break;
@@ -525,13 +542,15 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
                            tsb + 8 * Mma::word(kk), s > 0 || kk > 0);
           }
           tc_commit_pair(&empty[slot]);
+          if (s == stages - 1) tc_commit_pair(acc_full);
         }
-        if (ok) tc_commit_pair(acc_full);
+        __syncwarp();
       }
-      if (!ok) {                     // MMAs in flight end before the CTA does
-        tc_commit_pair(acc_full);
-        mbar_wait_drain(acc_full, done & 1);
-      }
+    }
+    if (!ok) {                       // MMAs in flight end before the CTA does
+      if (elect_one()) tc_commit_pair(acc_full);
+      __syncwarp();
+      mbar_wait_drain(acc_full, done & 1);
     }
     __syncwarp();
   } else if (warp >= 4) {
