@@ -81,6 +81,11 @@ __device__ __forceinline__ uint64_t make_sdesc_plain(uint32_t smem_addr) {
   return d;
 }
 
+// mbar_wait() by a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
+}
+
 struct MxMatmulParams {
   const uint8_t* sa;      // scale tiles of A [M] and B [N]
   const uint8_t* sb;
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     int issued = 0;
     for (int s = s0; s < s1; ++s) {
       const int i = s - s0, slot = i % T::kStages;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status))) break;
+      if (!warp_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status)) break;
       if (elect_one()) {
         uint8_t* st = smem + slot * T::kStageBytes;
         const uint32_t words = min((int)Mma::kWords, p.KT - s * (int)Mma::kWords);
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     const uint32_t qcol = (uint32_t)(q0 % 128) / 32;
     for (int s = s0; s < s1; ++s) {
       const int i = s - s0, slot = i % T::kStages;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status))) break;
+      if (!warp_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
       const uint32_t sf = st + T::kStageBytes - 2 * T::kSfBytes;
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   };
   float* part = reinterpret_cast<float*>(smem);              // [NT][128], over the drained stages
   if (warp >= 2) {
-    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(done, 0, abort_flag, p.status));
+    const bool ok = warp_wait(done, 0, abort_flag, p.status);
     tc_fence_after();
     if (ok) {
 #pragma unroll 1
@@ -333,44 +338,13 @@ __device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// Arrival on a barrier of the cluster.  Only tensor memory is handed over with
+// it (ordered by the tcgen05 fences around), so the order of ordinary memory
+// stays within the CTA: a release to the cluster waits for every outstanding
+// store, 1300 cycles in each tile's critical path.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// mbar_wait() for a barrier that the other CTA arrives on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                                  uint32_t* status) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 63u) == 63u) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        *abort_flag = 1;
-        atomicOr(status, kStatusTimeout);
-        return false;
-      }
-    }
-  }
-}
-
-// The same for a whole warp: one answer for all lanes.
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                                  uint32_t* status) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity, abort_flag, status));
-}
-
 // Tiled loads of a CTA pair: the destination is this CTA's, the barrier may
 // be the peer's (both given as shared addresses of the cluster).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x,
@@ -479,7 +453,7 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
       const int arow = mi * 256 + 128 * (int)rank, brow = ni * 256 + 128 * (int)rank;
       for (int s = 0; s < stages; ++s, ++i) {
         const int slot = i % T::kStages;
-        if (!(ok = warp_wait_cluster(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status))) break;
+        if (!(ok = warp_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status))) break;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[slot], T::kTxBytes);
           const uint32_t bar = mapa_u32(smem_u32(&full[slot]), 0);
@@ -497,7 +471,7 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
     // barriers: long done after two milliseconds)
     if (ok)
       for (int j = i > T::kStages ? i - T::kStages : 0; j < i; ++j)
-        if (!warp_wait_cluster(&empty[j % T::kStages], (j / T::kStages) & 1, abort_flag, p.status)) break;
+        if (!warp_wait(&empty[j % T::kStages], (j / T::kStages) & 1, abort_flag, p.status)) break;
     if (*abort_flag)
       for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
       }
@@ -514,10 +488,10 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
     bool ok = true;
     for (int64_t t = pair; ok && t < tiles; t += pairs, ++done) {
       // the last tile's sums have left tensor memory
-      if (!(ok = warp_wait_cluster(acc_free, (done & 1) ^ 1, abort_flag, p.status))) break;
+      if (!(ok = warp_wait(acc_free, (done & 1) ^ 1, abort_flag, p.status))) break;
       for (int s = 0; s < stages; ++s, ++i) {
         const int slot = i % T::kStages;
-        if (!(ok = warp_wait_cluster(&full[slot], (i / T::kStages) & 1, abort_flag, p.status))) break;
+        if (!(ok = warp_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status))) break;
         tc_fence_after();
         const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
         const uint32_t tsa = tmem + T::kColSf + slot * T::kSfCols, tsb = tsa + 4 * Mma::kWords;
@@ -576,7 +550,7 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
         bar_sync(1, 256);
       }
       const float ra = (p.ra != nullptr && row0 + lane < p.M) ? __ldg(p.ra + row0 + lane) : 1.0f;
-      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_full, done & 1, abort_flag, p.status));
+      ok = ok && warp_wait(acc_full, done & 1, abort_flag, p.status);
       if (!ok) continue;
       tc_fence_after();
       uint32_t u[4][32];
