@@ -564,48 +564,39 @@ MX_FORMATS = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
 _MX_MAX_ROWS, _MX_MAX_COLS = 1 << 24, 1 << 20
 
 
-class _on:
-    """The stream and device of a call: the tensors' device is made current and,
-    where a stream is given, outputs are allocated on it and the inputs marked
-    as used by it.  Gives the raw stream handle."""
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("stream", "context")
 
-    def __init__(self, device, stream, inputs):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        if stream is None and device.index == torch.cuda.current_device():
-            self.stream, self.context = torch.cuda.current_stream(device), None
-            return
-        other = stream is not None and stream != torch.cuda.current_stream(device)
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.context = torch.cuda.stream(self.stream)
-        if other:
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
-
-    def __enter__(self):
-        if self.context is not None:
-            self.context.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.context is not None:
-            self.context.__exit__(*exc)
+def _elsewhere(index: int, stream, inputs):
+    """None where a call is for the current device and stream.  Otherwise the
+    context that makes them so: the tensors' device becomes current, and where a
+    stream is given outputs are allocated on it and the inputs marked as used
+    by it."""
+    if stream is None:
+        return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _device_tensor(t, name: str, device=None) -> None:
+def _device_tensor(t, name: str, index: int = -1) -> int:
+    """The index of a CUDA tensor's device (the one given, if one is)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda:
+    got = t.get_device()
+    if got < 0 or not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+    if index >= 0 and got != index:
+        raise ValueError(f"{name}: expected a tensor on cuda:{index}, got one on {t.device}")
+    return got
 
 
 def _extent(t: torch.Tensor):
@@ -655,6 +646,7 @@ def _mx_format(fmt) -> int:
     return code
 
 
+@functools.lru_cache(maxsize=1024)
 def _mx_shapes(M: int, K: int, code: int):
     """Shapes of the codes and of the scale tiles of [M, K]."""
     if not 0 <= M <= _MX_MAX_ROWS or not 1 <= K <= _MX_MAX_COLS:
@@ -672,28 +664,30 @@ def alloc_microscaled(M: int, K: int, fmt: str, device) -> Microscaled:
                        torch.empty(M, dtype=torch.float32, device=device) if code == 2 else None, K, fmt)
 
 
-def _require_microscaled(q, name: str, device=None):
-    """(rows, format code) of a checked Microscaled."""
+def _require_microscaled(q, name: str, index: int = -1):
+    """(rows, format code, device index) of a checked Microscaled."""
     if not isinstance(q, Microscaled):
         raise TypeError(f"{name}: expected a Microscaled, got {type(q).__name__}")
-    code = _mx_format(q.fmt)
-    _device_tensor(q.codes, f"{name}.codes", device)
-    device = q.codes.device
-    if q.codes.dim() != 2:
+    codes, scales, row_scale, cols, fmt = q
+    code = _mx_format(fmt)
+    index = _device_tensor(codes, name + ".codes", index)
+    if codes.dim() != 2:
         raise ValueError(f"{name}.codes: expected a 2-D tensor")
-    M = q.codes.shape[0]
-    codes, scales = _mx_shapes(M, q.cols, code)
-    parts = [(q.codes, "codes", torch.uint8, codes), (q.scales, "scales", torch.uint8, scales)]
+    M = codes.shape[0]
+    code_shape, scale_shape = _mx_shapes(M, cols, code)
+    _device_tensor(scales, name + ".scales", index)
     if code == 2:
-        parts.append((q.row_scale, "row_scale", torch.float32, (M,)))
-    elif q.row_scale is not None:
-        raise ValueError(f"{name}.row_scale: {q.fmt} rows have none")
-    for t, part, dtype, shape in parts:
-        _device_tensor(t, f"{name}.{part}", device)
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}.{part}: expected a contiguous {dtype} tensor of shape {shape}, "
+        _device_tensor(row_scale, name + ".row_scale", index)
+        if row_scale.dtype != torch.float32 or row_scale.shape != (M,) or not row_scale.is_contiguous():
+            raise ValueError(f"{name}.row_scale: expected contiguous float32 [{M}], "
+                             f"got {row_scale.dtype} {tuple(row_scale.shape)}")
+    elif row_scale is not None:
+        raise ValueError(f"{name}.row_scale: {fmt} rows have none")
+    for t, part, shape in ((codes, "codes", code_shape), (scales, "scales", scale_shape)):
+        if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}.{part}: expected a contiguous uint8 tensor of shape {shape}, "
                              f"got {t.dtype} {tuple(t.shape)}")
-    return M, code
+    return M, code, index
 
 
 def _rows(x, name: str):
@@ -711,45 +705,51 @@ def _rows(x, name: str):
     return M, K, x.stride(0) if M > 1 else K
 
 
+def _require_mx_out(out, fmt: str, M: int, K: int, code: int, index: int, inputs) -> None:
+    if _require_microscaled(out, "out", index)[:2] != (M, code) or out.cols != K:
+        raise ValueError(f"out: expected {fmt} rows [{M}, {K}]")
+    for t in out[:3]:
+        if t is not None:
+            _apart(t, "out", inputs)
+
+
 def mx_quantize(x: torch.Tensor, fmt: str, out: Optional[Microscaled] = None, stream=None) -> Microscaled:
     """Rows [..., K] of bfloat16, float16 or float32 -> Microscaled rows (leading
     dimensions flattened).  A block (nvfp4: a row) with a NaN or an infinity
     stands for NaN."""
-    _device_tensor(x, "x")
+    index = _device_tensor(x, "x")
+    if (there := _elsewhere(index, stream, (x,))) is not None:
+        with there:
+            return mx_quantize(x, fmt, out)
     dtype, code = _float_dtype(x, "x"), _mx_format(fmt)
     M, K, ld = _rows(x, "x")
-    _mx_shapes(M, K, code)
-    if out is not None:
-        if _require_microscaled(out, "out", x.device) != (M, code) or out.cols != K:
-            raise ValueError(f"out: expected {fmt} rows [{M}, {K}]")
-        for t in out[:3]:
-            if t is not None:
-                _apart(t, "out", (x,))
-    with _on(x.device, stream, (x,)) as s:
-        if out is None:
-            out = alloc_microscaled(M, K, fmt, x.device)
-        _check(_load().fqa_mx_quantize(x.data_ptr(), dtype, M, K, ld, code, out.codes.data_ptr(),
-                                       out.scales.data_ptr(), _at(out.row_scale), s), "fqa_mx_quantize")
+    if out is None:
+        out = alloc_microscaled(M, K, fmt, x.device)
+    else:
+        _require_mx_out(out, fmt, M, K, code, index, (x,))
+    _check(_load().fqa_mx_quantize(x.data_ptr(), dtype, M, K, ld, code, out.codes.data_ptr(), out.scales.data_ptr(),
+                                   _at(out.row_scale), _raw_stream(index)), "fqa_mx_quantize")
     return out
 
 
 def mx_dequantize(q: Microscaled, out_dtype: int = FQA_OUT_BF16, out: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """The values that microscaled rows stand for, [M, cols]."""
-    M, code = _require_microscaled(q, "q")
+    M, code, index = _require_microscaled(q, "q")
+    if (there := _elsewhere(index, stream, q[:3])) is not None:
+        with there:
+            return mx_dequantize(q, out_dtype, out)
     dt = _OUT_DTYPE.get(out_dtype)
     if dt is None:
         raise ValueError(f"out_dtype: unknown value {out_dtype!r}")
-    device = q.codes.device
-    if out is not None:
-        _device_tensor(out, "out", device)
+    if out is None:
+        out = torch.empty((M, q.cols), dtype=dt, device=q.codes.device)
+    else:
+        _device_tensor(out, "out", index)
         _require(out, dt, "out", (M, q.cols))
         _apart(out, "out", q[:3])
-    with _on(device, stream, q[:3]) as s:
-        if out is None:
-            out = torch.empty(M, q.cols, dtype=dt, device=device)
-        _check(_load().fqa_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), _at(q.row_scale), M, q.cols, code,
-                                         out.data_ptr(), out_dtype, s), "fqa_mx_dequantize")
+    _check(_load().fqa_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), _at(q.row_scale), M, q.cols, code,
+                                     out.data_ptr(), out_dtype, _raw_stream(index)), "fqa_mx_dequantize")
     return out
 
 
@@ -760,43 +760,42 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, fmt: str = "mxfp8", resid
     [..., K]: (y as Microscaled rows, h in residual's type, or None without a
     residual).  weight [K] and residual are of x's type or float32.
     residual_out may be residual itself (or x, where of the same type)."""
-    _device_tensor(x, "x")
+    index = _device_tensor(x, "x")
+    if (there := _elsewhere(index, stream, (x, weight, residual))) is not None:
+        with there:
+            return mx_rms_norm(x, weight, fmt, residual, eps, out, residual_out)
     dtype, code = _float_dtype(x, "x"), _mx_format(fmt)
     M, K, ld = _rows(x, "x")
-    _mx_shapes(M, K, code)
-    _device_tensor(weight, "weight", x.device)
-    _require(weight, torch.float32 if weight.dtype == torch.float32 else x.dtype, "weight", (K,))
-    ldr = K
+    _device_tensor(weight, "weight", index)
+    if weight.shape != (K,) or weight.dtype not in (x.dtype, torch.float32) or not weight.is_contiguous():
+        raise ValueError(f"weight: expected contiguous [{K}] of {x.dtype} or float32, "
+                         f"got {tuple(weight.shape)} {weight.dtype}")
+    if not 0.0 <= eps < float("inf"):
+        raise ValueError(f"eps: expected a finite value of at least 0, got {eps}")
+    ldr, res_dtype = K, dtype
     if residual is not None:
-        _device_tensor(residual, "residual", x.device)
+        _device_tensor(residual, "residual", index)
         if residual.shape != x.shape or residual.dtype not in (x.dtype, torch.float32):
             raise ValueError(f"residual: expected {tuple(x.shape)} of {x.dtype} or float32, "
                              f"got {tuple(residual.shape)} {residual.dtype}")
-        ldr = _rows(residual, "residual")[2]
-        if residual_out is not None:
-            _device_tensor(residual_out, "residual_out", x.device)
+        ldr, res_dtype = _rows(residual, "residual")[2], _DTYPE[residual.dtype]
+        if residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+        else:
+            _device_tensor(residual_out, "residual_out", index)
             _require(residual_out, residual.dtype, "residual_out", x.shape)
             _apart(residual_out, "residual_out",
                    [weight] + [t for t in (x, residual) if not _same_memory(residual_out, t)])
     elif residual_out is not None:
         raise ValueError("residual_out: there is no residual")
-    if not 0.0 <= eps < float("inf"):
-        raise ValueError(f"eps: expected a finite value of at least 0, got {eps}")
-    if out is not None:
-        if _require_microscaled(out, "out", x.device) != (M, code) or out.cols != K:
-            raise ValueError(f"out: expected {fmt} rows [{M}, {K}]")
-        for t in out[:3]:
-            if t is not None:
-                _apart(t, "out", (x, weight, residual, residual_out))
-    with _on(x.device, stream, (x, weight, residual)) as s:
-        if out is None:
-            out = alloc_microscaled(M, K, fmt, x.device)
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
-        _check(_load().fqa_mx_rms_norm(
-            x.data_ptr(), dtype, M, K, ld, weight.data_ptr(), _DTYPE[weight.dtype], eps, _at(residual),
-            dtype if residual is None else _DTYPE[residual.dtype], ldr, code, out.codes.data_ptr(),
-            out.scales.data_ptr(), _at(out.row_scale), _at(residual_out), s), "fqa_mx_rms_norm")
+    if out is None:
+        out = alloc_microscaled(M, K, fmt, x.device)
+    else:
+        _require_mx_out(out, fmt, M, K, code, index, (x, weight, residual, residual_out))
+    _check(_load().fqa_mx_rms_norm(
+        x.data_ptr(), dtype, M, K, ld, weight.data_ptr(), _DTYPE[weight.dtype], eps, _at(residual), res_dtype, ldr, code,
+        out.codes.data_ptr(), out.scales.data_ptr(), _at(out.row_scale), _at(residual_out), _raw_stream(index)),
+        "fqa_mx_rms_norm")
     return out, residual_out
 
 
@@ -804,27 +803,28 @@ def mx_matmul(a: Microscaled, b: Microscaled, bias: Optional[torch.Tensor] = Non
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """a [M, K] times the transpose of b [N, K] (a projection's weights), both
     microscaled rows of one format, plus a float32 bias [N]: [M, N]."""
-    M, code = _require_microscaled(a, "a")
-    device = a.codes.device
-    N, other = _require_microscaled(b, "b", device)
+    M, code, index = _require_microscaled(a, "a")
+    N, other, _ = _require_microscaled(b, "b", index)
+    if (there := _elsewhere(index, stream, (*a[:3], *b[:3], bias))) is not None:
+        with there:
+            return mx_matmul(a, b, bias, out_dtype, out)
     if other != code or a.cols != b.cols:
         raise ValueError(f"a and b: {a.fmt} rows of {a.cols} against {b.fmt} rows of {b.cols}")
     dt = _OUT_DTYPE.get(out_dtype)
     if dt is None:
         raise ValueError(f"out_dtype: unknown value {out_dtype!r}")
     if bias is not None:
-        _device_tensor(bias, "bias", device)
+        _device_tensor(bias, "bias", index)
         _require(bias, torch.float32, "bias", (N,))
-    if out is not None:
-        _device_tensor(out, "out", device)
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=a.codes.device)
+    else:
+        _device_tensor(out, "out", index)
         _require(out, dt, "out", (M, N))
         _apart(out, "out", (*a[:3], *b[:3], bias))
-    with _on(device, stream, (*a[:3], *b[:3], bias)) as s:
-        if out is None:
-            out = torch.empty(M, N, dtype=dt, device=device)
-        _check(_load().fqa_mx_matmul(a.codes.data_ptr(), a.scales.data_ptr(), _at(a.row_scale), b.codes.data_ptr(),
-                                     b.scales.data_ptr(), _at(b.row_scale), _at(bias), M, N, a.cols, code,
-                                     out.data_ptr(), out_dtype, s), "fqa_mx_matmul")
+    _check(_load().fqa_mx_matmul(a.codes.data_ptr(), a.scales.data_ptr(), _at(a.row_scale), b.codes.data_ptr(),
+                                 b.scales.data_ptr(), _at(b.row_scale), _at(bias), M, N, a.cols, code, out.data_ptr(),
+                                 out_dtype, _raw_stream(index)), "fqa_mx_matmul")
     return out
 
 
@@ -861,58 +861,66 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary, inverse: boo
     adjacent channels; k may be None) -> both normalized (where rot has
     weights) and rotated, contiguous.  `inverse` rotates back.  An output may be
     its own input where that is contiguous."""
-    _device_tensor(q, "q")
-    device, dtype = q.device, _float_dtype(q, "q")
+    index = _device_tensor(q, "q")
+    if not isinstance(rot, Rotary):
+        raise TypeError(f"rot: expected a Rotary, got {type(rot).__name__}")
+    pos, axes, theta, split, shared, q_weight, k_weight, eps = rot
+    if (there := _elsewhere(index, stream, (q, k, pos, q_weight, k_weight))) is not None:
+        with there:
+            return rotary(q, k, rot, inverse, q_out, k_out)
+    dtype = _float_dtype(q, "q")
     if q.dim() != 4:
         raise ValueError("q: expected a [B, H, N, 128] tensor")
     B, Hq, N, d = q.shape
-    Hk = 0
+    if d != HEAD_DIM:
+        raise ValueError(f"q: expected {HEAD_DIM} channels, got {d}")
+    sb, sh, sn, sd = q.stride()
+    kb = kh = kn = Hk = 0
+    kd = 1
     if k is not None:
-        _device_tensor(k, "k", device)
+        _device_tensor(k, "k", index)
         if k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
             raise ValueError(f"k: expected [{B}, H, {N}, {d}] of {q.dtype}, got {tuple(k.shape)} {k.dtype}")
         Hk = k.shape[1]
+        kb, kh, kn, kd = k.stride()
     elif k_out is not None:
         raise ValueError("k_out: there is no k")
-    if d != HEAD_DIM:
-        raise ValueError(f"q: expected {HEAD_DIM} channels, got {d}")
-    for name, t in (("q", q), ("k", k)):
-        if t is not None and t.stride(3) != 1:
-            raise ValueError(f"{name}: expected adjacent channels, got stride {t.stride(3)}")
-    if not isinstance(rot, Rotary):
-        raise TypeError(f"rot: expected a Rotary, got {type(rot).__name__}")
-    axes = _axes_array(tuple(rot.axes), bool(rot.split))
-    pos, A = rot.positions, len(rot.axes)
-    _device_tensor(pos, "rot.positions", device)
+    if sd != 1 or kd != 1:
+        raise ValueError(f"q and k: expected adjacent channels, got strides {sd} and {kd}")
+    array, A = _axes_array(axes if isinstance(axes, tuple) else tuple(axes), bool(split)), len(axes)
+    _device_tensor(pos, "rot.positions", index)
+    shape = pos.shape
     if pos.dtype not in (torch.int32, torch.float32) or not pos.is_contiguous() or (
-            pos.shape != (N, A) and pos.shape != (B, N, A) and pos.shape != (1, N, A)):
+            shape != (N, A) and shape != (B, N, A) and shape != (1, N, A)):
         raise ValueError(f"rot.positions: expected contiguous int32 or float32 [{N}, {A}] or [{B}, {N}, {A}], "
-                         f"got {pos.dtype} {tuple(pos.shape)}")
-    for name, w in (("rot.q_weight", rot.q_weight), ("rot.k_weight", rot.k_weight)):
+                         f"got {pos.dtype} {tuple(shape)}")
+    for name, w in (("rot.q_weight", q_weight), ("rot.k_weight", k_weight)):
         if w is not None:
-            _device_tensor(w, name, device)
-            _require(w, q.dtype, name, (HEAD_DIM,))
-    if not 0.0 < rot.theta < float("inf") or not 0.0 <= rot.eps < float("inf"):
-        raise ValueError(f"rot: expected a finite theta > 0 and eps >= 0, got {rot.theta} and {rot.eps}")
-    inputs = (q, k, pos, rot.q_weight, rot.k_weight)
-    for name, o, own, others in (("q_out", q_out, q, inputs[1:]), ("k_out", k_out, k, (q, *inputs[2:]))):
-        if o is not None:
-            _device_tensor(o, name, device)
-            _require(o, q.dtype, name, own.shape)
-            _apart(o, name, others if _same_memory(o, own) else (own, *others))
-    if q_out is not None and k_out is not None:
-        _apart(k_out, "k_out", (q_out,))
-    with _on(device, stream, inputs) as s:
+            _device_tensor(w, name, index)
+            if w.dtype != q.dtype or w.shape != (HEAD_DIM,) or not w.is_contiguous():
+                raise ValueError(f"{name}: expected contiguous [{HEAD_DIM}] of {q.dtype}, got {w.dtype} {tuple(w.shape)}")
+    if not 0.0 < theta < float("inf") or not 0.0 <= eps < float("inf"):
+        raise ValueError(f"rot: expected a finite theta > 0 and eps >= 0, got {theta} and {eps}")
+    if q_out is None and k_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        weights = (pos, q_weight, k_weight)
+        for name, o, own, others in (("q_out", q_out, q, (k, *weights)), ("k_out", k_out, k, (q, *weights))):
+            if o is not None:
+                _device_tensor(o, name, index)
+                _require(o, q.dtype, name, own.shape)
+                _apart(o, name, others if _same_memory(o, own) else (own, *others))
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=device)
-        ks = (0, 0, 0) if k is None else k.stride()[:3]
-        _check(_load().fqa_rotary(
-            q.data_ptr(), _at(k), dtype, B, Hq, Hk, N, d, *q.stride()[:3], *ks, pos.data_ptr(), _DTYPE[pos.dtype],
-            N * A if pos.dim() == 3 and pos.shape[0] > 1 else 0, A, axes, rot.theta,
-            (1 if rot.split else 0) | (2 if rot.shared else 0) | (4 if inverse else 0), _at(rot.q_weight),
-            _at(rot.k_weight), rot.eps, q_out.data_ptr(), _at(k_out), s), "fqa_rotary")
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif k_out is not None:
+            _apart(k_out, "k_out", (q_out,))
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    _check(_load().fqa_rotary(
+        q.data_ptr(), _at(k), dtype, B, Hq, Hk, N, d, sb, sh, sn, kb, kh, kn, pos.data_ptr(), _DTYPE[pos.dtype],
+        N * A if len(shape) == 3 and shape[0] > 1 else 0, A, array, theta,
+        (1 if split else 0) | (2 if shared else 0) | (4 if inverse else 0), _at(q_weight), _at(k_weight), eps,
+        q_out.data_ptr(), _at(k_out), _raw_stream(index)), "fqa_rotary")
     return q_out, k_out
 
 
