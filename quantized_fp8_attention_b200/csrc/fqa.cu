@@ -246,54 +246,68 @@ static size_t dtype_bytes(int t) { return t == FQA_DTYPE_F32 ? 4 : 2; }
 
 // -------------------------------------------- launches of microscaled rows
 
-// One launch of the row kernel that fits the row: 8 elements a thread and
-// chunk, up to four chunks in registers.  Threads per row by K: a warp up to
-// 1024 elements (no block-wide sums), 128 up to 4096, 512 up to 16384, and
-// longer rows are read again for each step.
+// One launch of the row kernel that fits the row: 16 elements a thread and
+// chunk, two chunks in registers.  Threads per row by its length: a warp up to
+// 1024 elements (no block-wide sums), then 128, 256 and 512 up to 16384; longer
+// rows, and rows off the 16-byte boundaries, are read again for each step.
 template <typename T, int FMT, bool kNorm>
-static void launch_mx_rows(const MxRowParams& p, cudaStream_t s) {
-  const int width = p.KT * MxTraits<FMT>::kWordChunks * 8;
-  if (width <= 1024)
-    mx_row_kernel<T, FMT, kNorm, 32, 4, false><<<(p.M + 3) / 4, 128, 0, s>>>(p);
+static void launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s) {
+  const int width = p.KT * MxTraits<FMT>::kWordChunks * kMxChunk;
+  if (!vec)
+    mx_row_kernel<T, FMT, kNorm, 128, 1, true, false><<<p.M, 128, 0, s>>>(p);
+  else if (width <= 1024)
+    mx_row_kernel<T, FMT, kNorm, 32, 2, false, true><<<(p.M + 3) / 4, 128, 0, s>>>(p);
   else if (width <= 4096)
-    mx_row_kernel<T, FMT, kNorm, 128, 4, false><<<p.M, 128, 0, s>>>(p);
+    mx_row_kernel<T, FMT, kNorm, 128, 2, false, true><<<p.M, 128, 0, s>>>(p);
+  else if (width <= 8192)
+    mx_row_kernel<T, FMT, kNorm, 256, 2, false, true><<<p.M, 256, 0, s>>>(p);
   else if (width <= 16384)
-    mx_row_kernel<T, FMT, kNorm, 512, 4, false><<<p.M, 512, 0, s>>>(p);
+    mx_row_kernel<T, FMT, kNorm, 512, 2, false, true><<<p.M, 512, 0, s>>>(p);
   else
-    mx_row_kernel<T, FMT, kNorm, 512, 1, true><<<p.M, 512, 0, s>>>(p);
+    mx_row_kernel<T, FMT, kNorm, 512, 1, true, true><<<p.M, 512, 0, s>>>(p);
 }
 
 template <typename T, bool kNorm>
-static void launch_mx_format(const MxRowParams& p, int fmt, cudaStream_t s) {
+static void launch_mx_format(const MxRowParams& p, int fmt, bool vec, cudaStream_t s) {
   if (fmt == FQA_MXFP8)
-    launch_mx_rows<T, kMxFp8, kNorm>(p, s);
+    launch_mx_rows<T, kMxFp8, kNorm>(p, vec, s);
   else if (fmt == FQA_MXFP4)
-    launch_mx_rows<T, kMxFp4, kNorm>(p, s);
+    launch_mx_rows<T, kMxFp4, kNorm>(p, vec, s);
   else
-    launch_mx_rows<T, kNvFp4, kNorm>(p, s);
+    launch_mx_rows<T, kNvFp4, kNorm>(p, vec, s);
 }
 
 template <bool kNorm>
-static fqa_status launch_mx(const MxRowParams& p, int dtype, int fmt, cudaStream_t s) {
+static fqa_status launch_mx(const MxRowParams& p, int dtype, int fmt, bool vec, cudaStream_t s) {
   if (dtype == FQA_DTYPE_BF16)
-    launch_mx_format<__nv_bfloat16, kNorm>(p, fmt, s);
+    launch_mx_format<__nv_bfloat16, kNorm>(p, fmt, vec, s);
   else if (dtype == FQA_DTYPE_F16)
-    launch_mx_format<__half, kNorm>(p, fmt, s);
+    launch_mx_format<__half, kNorm>(p, fmt, vec, s);
   else
-    launch_mx_format<float, kNorm>(p, fmt, s);
+    launch_mx_format<float, kNorm>(p, fmt, vec, s);
   return launch_status();
 }
 
-template <typename T>
-static void launch_mx_dequantize(const MxDequantParams& p, int fmt, cudaStream_t s) {
-  const int64_t chunks = (int64_t)p.M * ((p.K + 7) / 8);
-  const int grid = (int)std::min<int64_t>((chunks + 255) / 256, 148 * 64);
-  if (fmt == FQA_MXFP8)
-    mx_dequantize_kernel<T, kMxFp8><<<grid, 256, 0, s>>>(p);
-  else if (fmt == FQA_MXFP4)
-    mx_dequantize_kernel<T, kMxFp4><<<grid, 256, 0, s>>>(p);
+template <typename T, int FMT>
+static void launch_mx_dequantize(const MxDequantParams& p, bool vec, cudaStream_t s) {
+  const int chunks = (p.K + kMxChunk - 1) / kMxChunk;
+  int tx = 4;                            // chunks side by side: a power of two, up to a whole CTA
+  while (tx < chunks && tx < 256) tx *= 2;
+  const dim3 block(tx, 256 / tx), grid((p.M + block.y - 1) / block.y);
+  if (vec)
+    mx_dequantize_kernel<T, FMT, true><<<grid, block, 0, s>>>(p);
   else
-    mx_dequantize_kernel<T, kNvFp4><<<grid, 256, 0, s>>>(p);
+    mx_dequantize_kernel<T, FMT, false><<<grid, block, 0, s>>>(p);
+}
+
+template <typename T>
+static void launch_mx_dequantize_format(const MxDequantParams& p, int fmt, bool vec, cudaStream_t s) {
+  if (fmt == FQA_MXFP8)
+    launch_mx_dequantize<T, kMxFp8>(p, vec, s);
+  else if (fmt == FQA_MXFP4)
+    launch_mx_dequantize<T, kMxFp4>(p, vec, s);
+  else
+    launch_mx_dequantize<T, kNvFp4>(p, vec, s);
 }
 
 template <int FMT, int NT>
@@ -772,9 +786,10 @@ size_t fqa_mx_scale_bytes(int M, int K, fqa_mx_format fmt) {
   return (size_t)((M + 127) / 128) * mx_words(K, fmt) * 512;
 }
 
-// Rows whose every start is 16-byte aligned and whose length is whole chunks.
+// Rows whose every start is 16-byte aligned and whose length is whole groups of
+// 16 bytes.
 static bool rows_vectorize(const void* base, int64_t ld, int K, size_t elt) {
-  return K % 8 == 0 && aligned(base, 16) && (ld * (int64_t)elt) % 16 == 0;
+  return K * elt % 16 == 0 && aligned(base, 16) && (ld * (int64_t)elt) % 16 == 0;
 }
 
 // The checks and fields common to both row calls.
@@ -795,7 +810,6 @@ static fqa_status mx_row_params(MxRowParams* p, const void* x, int dtype, int M,
   p->K = K;
   p->Kp = mx_padded(K);
   p->KT = mx_words(K, fmt);
-  p->vec_x = rows_vectorize(x, ldx, K, elt);
   p->codes = codes;
   p->scales = reinterpret_cast<uint32_t*>(scales);
   p->row_scale = row_scale;
@@ -807,7 +821,8 @@ fqa_status fqa_mx_quantize(const void* x, fqa_dtype dtype, int M, int K, int64_t
   MxRowParams p;
   const fqa_status st = mx_row_params(&p, x, dtype, M, K, ldx, fmt, codes, scales, row_scale);
   if (st != FQA_OK || M == 0) return st;
-  return launch_mx<false>(p, dtype, fmt, static_cast<cudaStream_t>(cuda_stream));
+  return launch_mx<false>(p, dtype, fmt, rows_vectorize(x, ldx, K, dtype_bytes(dtype)),
+                          static_cast<cudaStream_t>(cuda_stream));
 }
 
 fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t ldx, const void* weight,
@@ -828,17 +843,16 @@ fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t
     return FQA_ERR_MISALIGNED;
   p.weight = weight;
   p.w_f32 = weight_dtype == FQA_DTYPE_F32;
-  p.vec_w = rows_vectorize(weight, 0, K, welt);
+  bool vec = rows_vectorize(x, ldx, K, dtype_bytes(dtype)) && rows_vectorize(weight, 0, K, welt);
   p.eps = eps;
   p.residual = residual;
   p.residual_out = residual_out;
   if (res) {
     p.ldr = ldr;
     p.res_f32 = residual_dtype == FQA_DTYPE_F32;
-    p.vec_r = rows_vectorize(residual, ldr, K, relt);
-    p.vec_o = rows_vectorize(residual_out, K, K, relt);
+    vec = vec && rows_vectorize(residual, ldr, K, relt) && rows_vectorize(residual_out, K, K, relt);
   }
-  return launch_mx<true>(p, dtype, fmt, static_cast<cudaStream_t>(cuda_stream));
+  return launch_mx<true>(p, dtype, fmt, vec, static_cast<cudaStream_t>(cuda_stream));
 }
 
 fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int M, int K,
@@ -850,15 +864,15 @@ fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const 
   if (fmt == FQA_NVFP4 && row_scale == nullptr) return FQA_ERR_INVALID_ARG;
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(row_scale, 4) || !aligned(out, dtype_bytes(out_dtype)))
     return FQA_ERR_MISALIGNED;
-  MxDequantParams p{codes, scales, row_scale, out, M, K, mx_padded(K), mx_words(K, fmt),
-                    rows_vectorize(out, K, K, dtype_bytes(out_dtype))};
+  const MxDequantParams p{codes, scales, row_scale, out, M, K, mx_padded(K), mx_words(K, fmt)};
+  const bool vec = rows_vectorize(out, K, K, dtype_bytes(out_dtype));
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (out_dtype == FQA_DTYPE_BF16)
-    launch_mx_dequantize<__nv_bfloat16>(p, fmt, s);
+    launch_mx_dequantize_format<__nv_bfloat16>(p, fmt, vec, s);
   else if (out_dtype == FQA_DTYPE_F16)
-    launch_mx_dequantize<__half>(p, fmt, s);
+    launch_mx_dequantize_format<__half>(p, fmt, vec, s);
   else
-    launch_mx_dequantize<float>(p, fmt, s);
+    launch_mx_dequantize_format<float>(p, fmt, vec, s);
   return launch_status();
 }
 

@@ -35,7 +35,7 @@ enum MxFormat : int { kMxFp8 = 0, kMxFp4 = 1, kNvFp4 = 2 };
 template <int FMT>
 struct MxTraits {
   static constexpr int kBlock = FMT == kNvFp4 ? 16 : 32;     // elements per scale
-  static constexpr int kBlockChunks = kBlock / 8;            // threads (8 elements each) per scale
+  static constexpr int kBlockChunks = kBlock / 16;           // threads (16 elements each) per scale
   static constexpr int kWordChunks = 4 * kBlockChunks;       // threads per word of four scales
 };
 
@@ -129,39 +129,91 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[W]) {
   }
 }
 
-// Elements [c0, c0 + 8) of a row of K (zeros past K); `vec`: the row's start
-// is 16-byte aligned and K a multiple of 8, so a chunk is whole or absent.
-template <typename T>
-__device__ __forceinline__ void load_chunk(const T* row, int c0, int K, bool vec, float (&v)[8]) {
-  if (vec && c0 < K) {
-    load_vec<T, 8>(row + c0, v);
-  } else {
+// A thread's chunk of a row: 16 elements, as they lie in memory.  kVec: the row
+// starts on a 16-byte boundary and K fills whole 16-byte groups, so each group
+// is there or not; without branches, so that the loads of several chunks and
+// tensors are all in flight before the first is used.
+constexpr int kMxChunk = 16;
+
+template <typename T, bool kVec>
+struct MxRaw {
+  static constexpr int kGroup = 16 / sizeof(T);              // elements per 16 bytes
+  uint4 g[kMxChunk / kGroup];
+  __device__ __forceinline__ void load(const T* row, int c0, int K) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c0 + e < K ? to_f32<T>(row[c0 + e]) : 0.0f;
+    for (int i = 0; i < kMxChunk / kGroup; ++i) {
+      g[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c0 + i * kGroup < K) g[i] = *reinterpret_cast<const uint4*>(row + c0 + i * kGroup);
+    }
   }
-}
+  __device__ __forceinline__ void get(float (&v)[kMxChunk]) const {
+#pragma unroll
+    for (int i = 0; i < kMxChunk / kGroup; ++i) {
+      const uint32_t w[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+          v[4 * i + e] = __uint_as_float(w[e]);
+        } else {
+          const float2 f = unpack2<T>(w[e]);
+          v[8 * i + 2 * e] = f.x;
+          v[8 * i + 2 * e + 1] = f.y;
+        }
+      }
+    }
+  }
+};
 template <typename T>
-__device__ __forceinline__ void store_chunk(T* row, int c0, int K, bool vec, const float (&v)[8]) {
-  if (vec && c0 < K) {
-    store_vec<T, 8>(row + c0, v);
+struct MxRaw<T, false> {
+  T g[kMxChunk];
+  __device__ __forceinline__ void load(const T* row, int c0, int K) {
+#pragma unroll
+    for (int e = 0; e < kMxChunk; ++e) g[e] = c0 + e < K ? row[c0 + e] : from_f32<T>(0.0f);
+  }
+  __device__ __forceinline__ void get(float (&v)[kMxChunk]) const {
+#pragma unroll
+    for (int e = 0; e < kMxChunk; ++e) v[e] = to_f32<T>(g[e]);
+  }
+};
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_chunk(T* row, int c0, int K, const float (&v)[kMxChunk]) {
+  if constexpr (kVec) {
+    constexpr int G = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kMxChunk / G; ++i)
+      if (c0 + i * G < K) {
+        float part[G];
+#pragma unroll
+        for (int e = 0; e < G; ++e) part[e] = v[i * G + e];
+        store_vec<T, G>(row + c0 + i * G, part);
+      }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < kMxChunk; ++e)
       if (c0 + e < K) row[c0 + e] = from_f32<T>(v[e]);
   }
 }
 
 // ----------------------------------------------------------- the codes
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// Largest magnitude of three values, NaN if one is.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
-// Largest |v| of eight values as its bit pattern: ordered like the magnitude,
-// and at or above 0x7F800000 exactly when one of them is not finite.
-__device__ __forceinline__ uint32_t chunk_amax(const float (&v)[8]) {
-  uint32_t m = 0;
+// Largest |v| of a chunk as its bit pattern: ordered like the magnitude, and at
+// or above 0x7F800000 exactly when one of them is not finite.
+__device__ __forceinline__ uint32_t chunk_amax(const float (&v)[kMxChunk]) {
+  float m = amax3(v[0], v[1], v[2]), n = amax3(v[3], v[4], v[5]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, abs_bits(v[e]));
-  return m;
+  for (int e = 6; e < 14; e += 4) {
+    m = amax3(m, v[e], v[e + 1]);
+    n = amax3(n, v[e + 2], v[e + 3]);
+  }
+  return __float_as_uint(amax3(amax3(m, v[14], v[15]), n, n)) & 0x7FFFFFFFu;
 }
 
 // Exponent byte of the smallest power of two whose `largest` multiple
@@ -174,7 +226,7 @@ __device__ __forceinline__ int power_byte(uint32_t amax, int top, uint32_t part,
 // 2^(127 - byte) for 0 <= byte <= 253.
 __device__ __forceinline__ float inverse_power(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
   return e2m1x2(v[0], v[1]) | (e2m1x2(v[2], v[3]) << 8) | (e2m1x2(v[4], v[5]) << 16) | (e2m1x2(v[6], v[7]) << 24);
 }
 
@@ -187,62 +239,69 @@ struct MxRowParams {
   float eps;
   int M, K, Kp, KT;       // KT words of four scales per row
   int res_f32, w_f32;
-  int vec_x, vec_r, vec_o, vec_w;
   uint8_t* codes;         // [M, Kp] or [M, Kp / 2]
   uint32_t* scales;       // tiles, as words
   float* row_scale;       // [M] (nvfp4)
 };
 
-// Writes chunk c (elements [8c, 8c + 8)) of a row.  Called by whole warps with
-// consecutive c, so the threads of a scale and of a word are neighbours.
-// row_amax: the row's largest magnitude (nvfp4).
+// Writes chunk c (elements [16c, 16c + 16)) of a row whose codes and scale
+// words start at `codes` and `words`.  Called by whole warps with consecutive
+// c, so the threads of a scale and of a word are neighbours.  row_amax: the
+// row's largest magnitude (nvfp4).
 template <int FMT>
-__device__ __forceinline__ void emit_chunk(const MxRowParams& p, int row, int c, const float (&v)[8], uint32_t row_amax) {
+__device__ __forceinline__ void emit_chunk(const MxRowParams& p, uint8_t* codes, uint32_t* words, int c,
+                                           float (&v)[kMxChunk], uint32_t row_amax) {
   using F = MxTraits<FMT>;
   uint32_t amax = chunk_amax(v);
 #pragma unroll
   for (int o = 1; o < F::kBlockChunks; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-  uint32_t byte;
-  float q[8];
+  uint32_t byte = 0;
   if constexpr (FMT == kNvFp4) {
-    byte = 0;
     float hi = 0.0f, lo = 0.0f, inv = 0.0f;
     if (row_amax < 0x7F800000u) {
       inv = inverse_power(power_byte(row_amax, 11, 0x280000u, 1));
       byte = e4m3x2(__fdiv_rn(__uint_as_float(amax) * inv, 6.0f), 0.0f) & 0xFFu;
-      if (byte != 0) {
-        const float s = e4m3x2_to_f2(byte).x;
-        hi = __frcp_rz(s);             // rounded down: lo >= 0, so a zero keeps its sign below
-        lo = __fmul_rn(__fmaf_rn(-s, hi, 1.0f), hi);
-      }
     }
+    if (byte != 0) {
+      const float s = e4m3x2_to_f2(byte).x;
+      hi = __frcp_rz(s);               // rounded down: lo >= 0, so a zero keeps its sign below
+      lo = __fmul_rn(__fmaf_rn(-s, hi, 1.0f), hi);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float y = byte != 0 ? __fmul_rn(v[e], inv) : 0.0f;
-      q[e] = __fmaf_rn(y, hi, __fmul_rn(y, lo));
+      for (int e = 0; e < kMxChunk; ++e) {
+        const float y = __fmul_rn(v[e], inv);
+        v[e] = __fmaf_rn(y, hi, __fmul_rn(y, lo));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kMxChunk; ++e) v[e] = 0.0f;
     }
   } else {
     const bool finite = amax < 0x7F800000u;
     byte = finite ? (uint32_t)(FMT == kMxFp8 ? power_byte(amax, 8, 0x600000u, 0) : power_byte(amax, 2, 0x400000u, 0))
                   : 0xFFu;
-    const float inv = inverse_power(finite ? (int)byte : 0);
+    if (finite) {
+      const float inv = inverse_power((int)byte);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = finite ? __fmul_rn(v[e], inv) : 0.0f;
+      for (int e = 0; e < kMxChunk; ++e) v[e] = __fmul_rn(v[e], inv);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kMxChunk; ++e) v[e] = 0.0f;
+    }
   }
-  if (8 * c < p.Kp) {
+  if (kMxChunk * c < p.Kp) {
     if constexpr (FMT == kMxFp8)
-      *reinterpret_cast<uint2*>(p.codes + (size_t)row * p.Kp + 8 * (size_t)c) =
-          make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+      *reinterpret_cast<uint4*>(codes + kMxChunk * (size_t)c) =
+          make_uint4(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]), e4m3x4(v[8], v[9], v[10], v[11]),
+                     e4m3x4(v[12], v[13], v[14], v[15]));
     else
-      *reinterpret_cast<uint32_t*>(p.codes + (size_t)row * (p.Kp / 2) + 4 * (size_t)c) = e2m1x8(q);
+      *reinterpret_cast<uint2*>(codes + kMxChunk / 2 * (size_t)c) = make_uint2(e2m1x8(&v[0]), e2m1x8(&v[8]));
   }
   // the word of four scales: each scale's threads shift theirs into place
   uint32_t w = byte << (8 * ((c / F::kBlockChunks) & 3));
   w |= __shfl_xor_sync(0xFFFFFFFFu, w, F::kBlockChunks);
   w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * F::kBlockChunks);
   const int word = c / F::kWordChunks;
-  if (c % F::kWordChunks == 0 && word < p.KT)
-    p.scales[((size_t)(row >> 7) * p.KT + word) * 128 + (row & 31) * 4 + ((row >> 5) & 3)] = w;
+  if (c % F::kWordChunks == 0 && word < p.KT) words[(size_t)word * 128] = w;
 }
 
 // Reductions over the TPR threads of a row (one warp, or the whole CTA).
@@ -273,12 +332,12 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   return v;
 }
 
-// One row per TPR threads, NCH chunks of 8 elements each held in registers
-// (kLoop: rows longer than TPR * NCH * 8 are read again for each step
-// instead).  Normed: h = x + residual in binary32, residual_out = h rounded,
-// y = h / sqrt(mean h^2 + eps) * weight, and y is quantized (never h, so the
-// norm sees the sum before its rounding).
-template <typename T, int FMT, bool kNorm, int TPR, int NCH, bool kLoop>
+// One row per TPR threads, NCH chunks of 16 elements each held in registers
+// (kLoop: rows longer than TPR * NCH * 16, or not on vector boundaries, are
+// read again for each step instead).  Normed: h = x + residual in binary32,
+// residual_out = h rounded, y = h / sqrt(mean h^2 + eps) * weight, and y is
+// quantized (never h's rounding: the norm sees the sum itself).
+template <typename T, int FMT, bool kNorm, int TPR, int NCH, bool kLoop, bool kVec>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxRowParams p) {
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
   __shared__ float red_sum[TPR / 32];
@@ -288,52 +347,103 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
   if (row >= p.M) return;                       // whole warps (and, for TPR >= 128, no CTA)
   const T* x = static_cast<const T*>(p.x) + (int64_t)row * p.ldx;
   const bool res = kNorm && p.residual != nullptr;
+  uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
+  uint32_t* words = p.scales + (size_t)(row >> 7) * p.KT * 128 + (row & 31) * 4 + ((row >> 5) & 3);
 
-  auto load_h = [&](int c, float (&v)[8]) {
-    load_chunk<T>(x, 8 * c, p.K, p.vec_x, v);
-    if (res) {
-      float r[8];
-      if (p.res_f32)
-        load_chunk<float>(static_cast<const float*>(p.residual) + (int64_t)row * p.ldr, 8 * c, p.K, p.vec_r, r);
-      else
-        load_chunk<T>(static_cast<const T*>(p.residual) + (int64_t)row * p.ldr, 8 * c, p.K, p.vec_r, r);
+  auto add_residual = [&](const auto& raw, float (&v)[kMxChunk]) {
+    float r[kMxChunk];
+    raw.get(r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += r[e];
+    for (int e = 0; e < kMxChunk; ++e) v[e] = __fadd_rn(v[e], r[e]);
+  };
+  auto store_h = [&](int c, const float (&v)[kMxChunk]) {
+    if (p.res_f32)
+      store_chunk<float, kVec>(static_cast<float*>(p.residual_out) + (int64_t)row * p.K, kMxChunk * c, p.K, v);
+    else
+      store_chunk<T, kVec>(static_cast<T*>(p.residual_out) + (int64_t)row * p.K, kMxChunk * c, p.K, v);
+  };
+  // h of NCH chunks, loads first
+  auto load_h = [&](int c0, float (&v)[NCH][kMxChunk]) {
+    MxRaw<T, kVec> a[NCH];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) a[j].load(x, kMxChunk * (c0 + j * TPR), p.K);
+    if (!res) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) a[j].get(v[j]);
+    } else if (p.res_f32) {
+      const float* r = static_cast<const float*>(p.residual) + (int64_t)row * p.ldr;
+      MxRaw<float, kVec> b[NCH];
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) b[j].load(r, kMxChunk * (c0 + j * TPR), p.K);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        a[j].get(v[j]);
+        add_residual(b[j], v[j]);
+      }
+    } else {
+      const T* r = static_cast<const T*>(p.residual) + (int64_t)row * p.ldr;
+      MxRaw<T, kVec> b[NCH];
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) b[j].load(r, kMxChunk * (c0 + j * TPR), p.K);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        a[j].get(v[j]);
+        add_residual(b[j], v[j]);
+      }
     }
   };
-  auto store_h = [&](int c, const float (&v)[8]) {
-    if (p.res_f32)
-      store_chunk<float>(static_cast<float*>(p.residual_out) + (int64_t)row * p.K, 8 * c, p.K, p.vec_o, v);
-    else
-      store_chunk<T>(static_cast<T*>(p.residual_out) + (int64_t)row * p.K, 8 * c, p.K, p.vec_o, v);
-  };
-  auto normed = [&](int c, float rstd, float (&v)[8]) {
-    float w[8];
-    if (p.w_f32)
-      load_chunk<float>(static_cast<const float*>(p.weight), 8 * c, p.K, p.vec_w, w);
-    else
-      load_chunk<T>(static_cast<const T*>(p.weight), 8 * c, p.K, p.vec_w, w);
+  auto squares = [&](const float (&v)[kMxChunk]) {
+    // four sums of four: short chains keep the rounding small
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 8 * c + e < p.K ? v[e] * rstd * w[e] : 0.0f;   // (no 0 * inf past K)
+    for (int e = 0; e < kMxChunk; ++e) s[e & 3] = __fmaf_rn(v[e], v[e], s[e & 3]);
+    return (s[0] + s[1]) + (s[2] + s[3]);
+  };
+  auto scaled = [&](int c, float rstd, const float (&w)[kMxChunk], float (&v)[kMxChunk]) {
+#pragma unroll
+    for (int e = 0; e < kMxChunk; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], rstd), w[e]);
+    if (kMxChunk * c + kMxChunk > p.K) {         // past K: not 0 * infinity
+#pragma unroll
+      for (int e = 0; e < kMxChunk; ++e)
+        if (kMxChunk * c + e >= p.K) v[e] = 0.0f;
+    }
+  };
+  auto inverse_root = [&](float ss) { return __frsqrt_rn(__fdiv_rn(row_sum<TPR>(ss, red_sum), (float)p.K) + p.eps); };
+  auto store_row_scale = [&](uint32_t amax) {
+    if (FMT == kNvFp4 && t == 0)
+      p.row_scale[row] = __uint_as_float(
+          amax < 0x7F800000u ? (uint32_t)power_byte(amax, 11, 0x280000u, 1) << 23 : 0x7FC00000u);
   };
 
   if constexpr (!kLoop) {
-    float v[NCH][8];
-    float ss = 0.0f;
+    float v[NCH][kMxChunk];
+    MxRaw<T, kVec> w[NCH];                       // the weights ride along with the row's loads
+    if (kNorm && !p.w_f32) {
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) load_h(t + j * TPR, v[j]);
+      for (int j = 0; j < NCH; ++j) w[j].load(static_cast<const T*>(p.weight), kMxChunk * (t + j * TPR), p.K);
+    }
+    load_h(t, v);
     if constexpr (kNorm) {
+      float ss = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NCH; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss += v[j][e] * v[j][e];
+      for (int j = 0; j < NCH; ++j) ss += squares(v[j]);
       if (res) {
 #pragma unroll
         for (int j = 0; j < NCH; ++j) store_h(t + j * TPR, v[j]);
       }
-      const float rstd = rsqrtf(__fdiv_rn(row_sum<TPR>(ss, red_sum), (float)p.K) + p.eps);
+      const float rstd = inverse_root(ss);
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) normed(t + j * TPR, rstd, v[j]);
+      for (int j = 0; j < NCH; ++j) {
+        float f[kMxChunk];
+        if (p.w_f32) {
+          MxRaw<float, kVec> g;
+          g.load(static_cast<const float*>(p.weight), kMxChunk * (t + j * TPR), p.K);
+          g.get(f);
+        } else {
+          w[j].get(f);
+        }
+        scaled(t + j * TPR, rstd, f, v[j]);
+      }
     }
     uint32_t amax = 0;
     if constexpr (FMT == kNvFp4) {
@@ -342,46 +452,53 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
       amax = row_max<TPR>(amax, red_max);
     }
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) emit_chunk<FMT>(p, row, t + j * TPR, v[j], amax);
-    if (FMT == kNvFp4 && t == 0)
-      p.row_scale[row] = amax < 0x7F800000u ? __uint_as_float((uint32_t)power_byte(amax, 11, 0x280000u, 1) << 23)
-                                            : __uint_as_float(0x7FC00000u);
+    for (int j = 0; j < NCH; ++j) emit_chunk<FMT>(p, codes, words, t + j * TPR, v[j], amax);
+    store_row_scale(amax);
   } else {
+    static_assert(NCH == 1, "one chunk per pass");
     // a whole number of passes for every thread: the shuffles need full warps
     const int passes = (p.KT * MxTraits<FMT>::kWordChunks + TPR - 1) / TPR;
+    auto normed = [&](int c, float rstd, float (&v)[kMxChunk]) {
+      float f[kMxChunk];
+      if (p.w_f32) {
+        MxRaw<float, kVec> g;
+        g.load(static_cast<const float*>(p.weight), kMxChunk * c, p.K);
+        g.get(f);
+      } else {
+        MxRaw<T, kVec> g;
+        g.load(static_cast<const T*>(p.weight), kMxChunk * c, p.K);
+        g.get(f);
+      }
+      scaled(c, rstd, f, v);
+    };
+    float v[1][kMxChunk];
     float rstd = 1.0f;
     if constexpr (kNorm) {
       float ss = 0.0f;
       for (int i = 0; i < passes; ++i) {
-        float v[8];
         load_h(t + i * TPR, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+        ss += squares(v[0]);
       }
-      rstd = rsqrtf(__fdiv_rn(row_sum<TPR>(ss, red_sum), (float)p.K) + p.eps);
+      rstd = inverse_root(ss);
     }
     uint32_t amax = 0;
     if constexpr (FMT == kNvFp4) {
       for (int i = 0; i < passes; ++i) {
-        float v[8];
         load_h(t + i * TPR, v);
-        if constexpr (kNorm) normed(t + i * TPR, rstd, v);
-        amax = max(amax, chunk_amax(v));
+        if constexpr (kNorm) normed(t + i * TPR, rstd, v[0]);
+        amax = max(amax, chunk_amax(v[0]));
       }
       amax = row_max<TPR>(amax, red_max);
     }
     // residual_out may be residual itself: each thread writes an element only
     // here, after its own last read of it
     for (int i = 0; i < passes; ++i) {
-      float v[8];
       load_h(t + i * TPR, v);
-      if (res) store_h(t + i * TPR, v);
-      if constexpr (kNorm) normed(t + i * TPR, rstd, v);
-      emit_chunk<FMT>(p, row, t + i * TPR, v, amax);
+      if (res) store_h(t + i * TPR, v[0]);
+      if constexpr (kNorm) normed(t + i * TPR, rstd, v[0]);
+      emit_chunk<FMT>(p, codes, words, t + i * TPR, v[0], amax);
     }
-    if (FMT == kNvFp4 && t == 0)
-      p.row_scale[row] = amax < 0x7F800000u ? __uint_as_float((uint32_t)power_byte(amax, 11, 0x280000u, 1) << 23)
-                                            : __uint_as_float(0x7FC00000u);
+    store_row_scale(amax);
   }
 }
 
@@ -405,44 +522,46 @@ struct MxDequantParams {
   const float* row_scale;
   void* out;              // contiguous [M, K]
   int M, K, Kp, KT;
-  int vec;                // K a multiple of 8: whole chunks, 16-byte aligned
 };
 
 // value = element * scale (exact in binary32) * row scale, rounded once more to
-// the output's type.  One thread per chunk of 8 elements.
-template <typename T, int FMT>
+// the output's type.  A thread takes chunks of 16 elements, blockDim.x of them
+// side by side in a row and blockDim.y rows per CTA (no division per chunk).
+template <typename T, int FMT, bool kVec>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParams p) {
   constexpr int kBlock = MxTraits<FMT>::kBlock;
-  const int chunks = (p.K + 7) / 8;
-  const int64_t total = (int64_t)p.M * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int row = (int)(i / chunks), c = (int)(i - (int64_t)row * chunks);
-    const int blk = 8 * c / kBlock;
-    const uint32_t sb = p.scales[((size_t)(row >> 7) * p.KT + (blk >> 2)) * 512 + (row & 31) * 16 +
-                                 ((row >> 5) & 3) * 4 + (blk & 3)];
-    float v[8];
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= p.M) return;
+  const uint8_t* sf = p.scales + (size_t)(row >> 7) * p.KT * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+  const uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
+  const float rs = FMT == kNvFp4 ? __ldg(p.row_scale + row) : 1.0f;
+  T* out = static_cast<T*>(p.out) + (int64_t)row * p.K;
+  for (int c = threadIdx.x; kMxChunk * c < p.K; c += blockDim.x) {
+    const int blk = kMxChunk * c / kBlock;
+    const uint32_t sb = sf[(size_t)(blk >> 2) * 512 + (blk & 3)];
+    float v[kMxChunk];
     if constexpr (FMT == kMxFp8) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p.codes + (size_t)row * p.Kp + 8 * (size_t)c);
+      const uint4 g = *reinterpret_cast<const uint4*>(codes + kMxChunk * (size_t)c);
+      const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = e4m3x2_to_f2(((e < 2 ? w.x : w.y) >> (16 * (e & 1))) & 0xFFFFu);
+      for (int e = 0; e < 8; ++e) {
+        const float2 f = e4m3x2_to_f2((w[e / 2] >> (16 * (e & 1))) & 0xFFFFu);
         v[2 * e] = f.x;
         v[2 * e + 1] = f.y;
       }
     } else {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(p.codes + (size_t)row * (p.Kp / 2) + 4 * (size_t)c);
+      const uint2 g = *reinterpret_cast<const uint2*>(codes + kMxChunk / 2 * (size_t)c);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = e2m1x2_to_f2((w >> (8 * e)) & 0xFFu);
+      for (int e = 0; e < 8; ++e) {
+        const float2 f = e2m1x2_to_f2(((e < 4 ? g.x : g.y) >> (8 * (e & 3))) & 0xFFu);
         v[2 * e] = f.x;
         v[2 * e + 1] = f.y;
       }
     }
     const float s = FMT == kNvFp4 ? e4m3x2_to_f2(sb).x : e8m0_to_f32(sb);
-    const float rs = FMT == kNvFp4 ? __ldg(p.row_scale + row) : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = FMT == kNvFp4 ? v[e] * s * rs : v[e] * s;
-    store_chunk<T>(static_cast<T*>(p.out) + (int64_t)row * p.K, 8 * c, p.K, p.vec, v);
+    for (int e = 0; e < kMxChunk; ++e) v[e] = FMT == kNvFp4 ? v[e] * s * rs : v[e] * s;
+    store_chunk<T, kVec>(out, kMxChunk * c, p.K, v);
   }
 }
 

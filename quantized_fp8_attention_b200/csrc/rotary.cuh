@@ -42,12 +42,55 @@ struct RotaryParams {
   uint8_t axis[64];
 };
 
+// A lane's two pieces of four channels of a row, as they lie in memory.
+template <typename T>
+struct RotRaw {
+  uint32_t w[2 * sizeof(T)];
+  template <bool kSplit>
+  __device__ __forceinline__ void load(const T* row, int c0, int c1, bool here) {
+#pragma unroll
+    for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[i] = 0u;
+    if (!here) return;
+    if constexpr (sizeof(T) == 4) {
+      const uint4 a = *reinterpret_cast<const uint4*>(row + c0), b = *reinterpret_cast<const uint4*>(row + c1);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else if constexpr (kSplit) {
+      const uint2 a = *reinterpret_cast<const uint2*>(row + c0), b = *reinterpret_cast<const uint2*>(row + c1);
+      w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(row + c0);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    }
+  }
+  __device__ __forceinline__ void load_elements(const T* row, int c0, int c1, bool here) {
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = here ? row[(i < 4 ? c0 : c1 - 4) + i] : from_f32<T>(0.0f);
+#pragma unroll
+    for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[i] = reinterpret_cast<const uint32_t*>(e)[i];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<T>(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+};
+
 // kSplit: pair j is channels (j, pairs + j); otherwise (2j, 2j + 1).  Lane l
 // holds two pieces of four channels: interleaved the neighbours [8l, 8l + 8),
 // split [4l, 4l + 4) and the four partners at pairs + 4l, so that a pair
 // never crosses lanes and each lane forms four angles.
 template <typename T, bool kSplit>
-__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(256, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
   const int l = threadIdx.x & 15;
   const int64_t token = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   const bool here = token < (int64_t)p.B * p.N;
@@ -95,53 +138,36 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
     const bool vec = p.vec[part];
     auto rows = [&](auto count, int h) {
       constexpr int U = decltype(count)::value;
-      float v[U][8];
+      // all loads first, kept as they lie in memory until used
+      RotRaw<T> raw[U];
+      if (vec) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const T* src = in + (int64_t)(h + u - base) * p.sh[part];
-        if (!here) {
+        for (int u = 0; u < U; ++u) raw[u].template load<kSplit>(in + (int64_t)(h + u - base) * p.sh[part], c0, c1, here);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
-        } else if (vec) {
-          if constexpr (!kSplit) {
-            load_vec<T, 8>(src + c0, v[u]);
-          } else {
-            float a[4], d[4];
-            load_vec<T, 4>(src + c0, a);
-            load_vec<T, 4>(src + c1, d);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[u][e] = a[e];
-              v[u][4 + e] = d[e];
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[u][e] = to_f32<T>(src[c0 + e]);
-            v[u][4 + e] = to_f32<T>(src[c1 + e]);
-          }
-        }
+        for (int u = 0; u < U; ++u) raw[u].load_elements(in + (int64_t)(h + u - base) * p.sh[part], c0, c1, here);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        float v[8];
+        raw[u].get(v);
         if (norm) {
           float ss = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss += v[u][e] * v[u][e];
+          for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
           const float r = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[u][e] = v[u][e] * r * w[e];
+          for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
         }
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int a = kSplit ? i : 2 * i, d = kSplit ? 4 + i : 2 * i + 1;
           const bool on = kSplit ? rotates : 4 * l + i < p.pairs;
-          y[a] = on ? v[u][a] * cs[i] - v[u][d] * sn[i] : v[u][a];
-          y[d] = on ? v[u][a] * sn[i] + v[u][d] * cs[i] : v[u][d];
+          y[a] = on ? v[a] * cs[i] - v[d] * sn[i] : v[a];
+          y[d] = on ? v[a] * sn[i] + v[d] * cs[i] : v[d];
         }
         if (here) {
           T* dst = out + (int64_t)(h + u - base) * p.N * kHeadDim;
