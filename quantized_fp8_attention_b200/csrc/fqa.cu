@@ -786,10 +786,12 @@ size_t fqa_mx_scale_bytes(int M, int K, fqa_mx_format fmt) {
   return (size_t)((M + 127) / 128) * mx_words(K, fmt) * 512;
 }
 
-// Rows whose every start is 16-byte aligned and whose length is whole groups of
-// 16 bytes.
-static bool rows_vectorize(const void* base, int64_t ld, int K, size_t elt) {
-  return K * elt % 16 == 0 && aligned(base, 16) && (ld * (int64_t)elt) % 16 == 0;
+// The widest access, 32 or 16 bytes (or 0), that every row's start and length
+// are multiples of.
+static int rows_vectorize(const void* base, int64_t ld, int K, size_t elt) {
+  for (int w : {32, 16})
+    if (K * elt % w == 0 && aligned(base, w) && (ld * (int64_t)elt) % w == 0) return w;
+  return 0;
 }
 
 // The checks and fields common to both row calls.
@@ -821,8 +823,9 @@ fqa_status fqa_mx_quantize(const void* x, fqa_dtype dtype, int M, int K, int64_t
   MxRowParams p;
   const fqa_status st = mx_row_params(&p, x, dtype, M, K, ldx, fmt, codes, scales, row_scale);
   if (st != FQA_OK || M == 0) return st;
-  return launch_mx<false>(p, dtype, fmt, rows_vectorize(x, ldx, K, dtype_bytes(dtype)),
-                          static_cast<cudaStream_t>(cuda_stream));
+  const int vec = rows_vectorize(x, ldx, K, dtype_bytes(dtype));
+  p.wide = vec == 32;
+  return launch_mx<false>(p, dtype, fmt, vec != 0, static_cast<cudaStream_t>(cuda_stream));
 }
 
 fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t ldx, const void* weight,
@@ -843,16 +846,17 @@ fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t
     return FQA_ERR_MISALIGNED;
   p.weight = weight;
   p.w_f32 = weight_dtype == FQA_DTYPE_F32;
-  bool vec = rows_vectorize(x, ldx, K, dtype_bytes(dtype)) && rows_vectorize(weight, 0, K, welt);
+  int vec = std::min(rows_vectorize(x, ldx, K, dtype_bytes(dtype)), rows_vectorize(weight, 0, K, welt));
   p.eps = eps;
   p.residual = residual;
   p.residual_out = residual_out;
   if (res) {
     p.ldr = ldr;
     p.res_f32 = residual_dtype == FQA_DTYPE_F32;
-    vec = vec && rows_vectorize(residual, ldr, K, relt) && rows_vectorize(residual_out, K, K, relt);
+    vec = std::min({vec, rows_vectorize(residual, ldr, K, relt), rows_vectorize(residual_out, K, K, relt)});
   }
-  return launch_mx<true>(p, dtype, fmt, vec, static_cast<cudaStream_t>(cuda_stream));
+  p.wide = vec == 32;
+  return launch_mx<true>(p, dtype, fmt, vec != 0, static_cast<cudaStream_t>(cuda_stream));
 }
 
 fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int M, int K,
@@ -864,15 +868,15 @@ fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const 
   if (fmt == FQA_NVFP4 && row_scale == nullptr) return FQA_ERR_INVALID_ARG;
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(row_scale, 4) || !aligned(out, dtype_bytes(out_dtype)))
     return FQA_ERR_MISALIGNED;
-  const MxDequantParams p{codes, scales, row_scale, out, M, K, mx_padded(K), mx_words(K, fmt)};
-  const bool vec = rows_vectorize(out, K, K, dtype_bytes(out_dtype));
+  const int vec = rows_vectorize(out, K, K, dtype_bytes(out_dtype));
+  const MxDequantParams p{codes, scales, row_scale, out, M, K, mx_padded(K), mx_words(K, fmt), vec == 32};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (out_dtype == FQA_DTYPE_BF16)
-    launch_mx_dequantize_format<__nv_bfloat16>(p, fmt, vec, s);
+    launch_mx_dequantize_format<__nv_bfloat16>(p, fmt, vec != 0, s);
   else if (out_dtype == FQA_DTYPE_F16)
-    launch_mx_dequantize_format<__half>(p, fmt, vec, s);
+    launch_mx_dequantize_format<__half>(p, fmt, vec != 0, s);
   else
-    launch_mx_dequantize_format<float>(p, fmt, vec, s);
+    launch_mx_dequantize_format<float>(p, fmt, vec != 0, s);
   return launch_status();
 }
 
@@ -973,13 +977,13 @@ fqa_status fqa_rotary(const void* q, const void* k, fqa_dtype dtype, int B, int 
       p.axis[j] = (uint8_t)a;
     }
   // groups of 16 lanes per token; with few tokens the heads are shared out
-  // to more groups (each forms its token's angles again) until about eight
-  // CTAs per SM have work
+  // to more groups, in batches of four (each forms its token's angles again),
+  // until about eight CTAs per SM have work
   fqa_status st = FQA_OK;
   if (!status_ptr(&st)) return st;
   const int64_t blocks = ((int64_t)B * N + 15) / 16;
   int64_t chunks = std::min<int64_t>(total, std::max<int64_t>(1, 8LL * num_sms() / blocks));
-  p.heads_per_group = (int)((total + chunks - 1) / chunks);
+  p.heads_per_group = (int)((total + chunks - 1) / chunks + 3) / 4 * 4;
   const dim3 grid((unsigned)blocks, (unsigned)((total + p.heads_per_group - 1) / p.heads_per_group));
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   using Fn = void (*)(const RotaryParams);

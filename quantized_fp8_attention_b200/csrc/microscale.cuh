@@ -129,21 +129,42 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[W]) {
   }
 }
 
+// 32 bytes per thread in one access (sm_100; address on a 32-byte boundary):
+// a whole sector, where two 16-byte stores of a thread would each write half
+// of one.
+__device__ __forceinline__ void load_32b(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void store_32b(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // A thread's chunk of a row: 16 elements, as they lie in memory.  kVec: the row
 // starts on a 16-byte boundary and K fills whole 16-byte groups, so each group
-// is there or not; without branches, so that the loads of several chunks and
-// tensors are all in flight before the first is used.
+// is there or not (`wide`: the same in 32 bytes).  Nothing here uses what it
+// loads, so that the loads of several chunks and tensors are all in flight
+// before the first is needed.
 constexpr int kMxChunk = 16;
 
 template <typename T, bool kVec>
 struct MxRaw {
   static constexpr int kGroup = 16 / sizeof(T);              // elements per 16 bytes
   uint4 g[kMxChunk / kGroup];
-  __device__ __forceinline__ void load(const T* row, int c0, int K) {
+  __device__ __forceinline__ void load(const T* row, int c0, int K, bool wide) {
 #pragma unroll
-    for (int i = 0; i < kMxChunk / kGroup; ++i) {
-      g[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (c0 + i * kGroup < K) g[i] = *reinterpret_cast<const uint4*>(row + c0 + i * kGroup);
+    for (int i = 0; i < kMxChunk / kGroup; ++i) g[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < kMxChunk / kGroup; i += 2)
+        if (c0 + i * kGroup < K) load_32b(row + c0 + i * kGroup, g[i], g[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMxChunk / kGroup; ++i)
+        if (c0 + i * kGroup < K) g[i] = *reinterpret_cast<const uint4*>(row + c0 + i * kGroup);
     }
   }
   __device__ __forceinline__ void get(float (&v)[kMxChunk]) const {
@@ -166,7 +187,7 @@ struct MxRaw {
 template <typename T>
 struct MxRaw<T, false> {
   T g[kMxChunk];
-  __device__ __forceinline__ void load(const T* row, int c0, int K) {
+  __device__ __forceinline__ void load(const T* row, int c0, int K, bool) {
 #pragma unroll
     for (int e = 0; e < kMxChunk; ++e) g[e] = c0 + e < K ? row[c0 + e] : from_f32<T>(0.0f);
   }
@@ -176,18 +197,39 @@ struct MxRaw<T, false> {
   }
 };
 
+// N values of T as words.
+template <typename T, int N>
+__device__ __forceinline__ void pack_words(const float* v, uint32_t (&w)[N * sizeof(T) / 4]) {
+#pragma unroll
+  for (int i = 0; i < (int)(N * sizeof(T) / 4); ++i) {
+    if constexpr (sizeof(T) == 4)
+      w[i] = __float_as_uint(v[i]);
+    else
+      w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+  }
+}
+
 template <typename T, bool kVec>
-__device__ __forceinline__ void store_chunk(T* row, int c0, int K, const float (&v)[kMxChunk]) {
+__device__ __forceinline__ void store_chunk(T* row, int c0, int K, bool wide, const float (&v)[kMxChunk]) {
   if constexpr (kVec) {
     constexpr int G = 16 / sizeof(T);
+    if (wide) {
 #pragma unroll
-    for (int i = 0; i < kMxChunk / G; ++i)
-      if (c0 + i * G < K) {
-        float part[G];
+      for (int i = 0; i < kMxChunk / G; i += 2)
+        if (c0 + i * G < K) {
+          uint32_t w[8];
+          pack_words<T, 2 * G>(&v[i * G], w);
+          store_32b(row + c0 + i * G, w);
+        }
+    } else {
 #pragma unroll
-        for (int e = 0; e < G; ++e) part[e] = v[i * G + e];
-        store_vec<T, G>(row + c0 + i * G, part);
-      }
+      for (int i = 0; i < kMxChunk / G; ++i)
+        if (c0 + i * G < K) {
+          uint32_t w[4];
+          pack_words<T, G>(&v[i * G], w);
+          *reinterpret_cast<uint4*>(row + c0 + i * G) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < kMxChunk; ++e)
@@ -239,6 +281,7 @@ struct MxRowParams {
   float eps;
   int M, K, Kp, KT;       // KT words of four scales per row
   int res_f32, w_f32;
+  int wide;               // every row on 32-byte boundaries, in whole groups of 32 bytes
   uint8_t* codes;         // [M, Kp] or [M, Kp / 2]
   uint32_t* scales;       // tiles, as words
   float* row_scale;       // [M] (nvfp4)
@@ -358,15 +401,15 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
   };
   auto store_h = [&](int c, const float (&v)[kMxChunk]) {
     if (p.res_f32)
-      store_chunk<float, kVec>(static_cast<float*>(p.residual_out) + (int64_t)row * p.K, kMxChunk * c, p.K, v);
+      store_chunk<float, kVec>(static_cast<float*>(p.residual_out) + (int64_t)row * p.K, kMxChunk * c, p.K, p.wide, v);
     else
-      store_chunk<T, kVec>(static_cast<T*>(p.residual_out) + (int64_t)row * p.K, kMxChunk * c, p.K, v);
+      store_chunk<T, kVec>(static_cast<T*>(p.residual_out) + (int64_t)row * p.K, kMxChunk * c, p.K, p.wide, v);
   };
   // h of NCH chunks, loads first
   auto load_h = [&](int c0, float (&v)[NCH][kMxChunk]) {
     MxRaw<T, kVec> a[NCH];
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) a[j].load(x, kMxChunk * (c0 + j * TPR), p.K);
+    for (int j = 0; j < NCH; ++j) a[j].load(x, kMxChunk * (c0 + j * TPR), p.K, p.wide);
     if (!res) {
 #pragma unroll
       for (int j = 0; j < NCH; ++j) a[j].get(v[j]);
@@ -374,7 +417,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
       const float* r = static_cast<const float*>(p.residual) + (int64_t)row * p.ldr;
       MxRaw<float, kVec> b[NCH];
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) b[j].load(r, kMxChunk * (c0 + j * TPR), p.K);
+      for (int j = 0; j < NCH; ++j) b[j].load(r, kMxChunk * (c0 + j * TPR), p.K, p.wide);
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         a[j].get(v[j]);
@@ -384,7 +427,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
       const T* r = static_cast<const T*>(p.residual) + (int64_t)row * p.ldr;
       MxRaw<T, kVec> b[NCH];
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) b[j].load(r, kMxChunk * (c0 + j * TPR), p.K);
+      for (int j = 0; j < NCH; ++j) b[j].load(r, kMxChunk * (c0 + j * TPR), p.K, p.wide);
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         a[j].get(v[j]);
@@ -420,7 +463,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
     MxRaw<T, kVec> w[NCH];                       // the weights ride along with the row's loads
     if (kNorm && !p.w_f32) {
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) w[j].load(static_cast<const T*>(p.weight), kMxChunk * (t + j * TPR), p.K);
+      for (int j = 0; j < NCH; ++j) w[j].load(static_cast<const T*>(p.weight), kMxChunk * (t + j * TPR), p.K, p.wide);
     }
     load_h(t, v);
     if constexpr (kNorm) {
@@ -437,7 +480,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
         float f[kMxChunk];
         if (p.w_f32) {
           MxRaw<float, kVec> g;
-          g.load(static_cast<const float*>(p.weight), kMxChunk * (t + j * TPR), p.K);
+          g.load(static_cast<const float*>(p.weight), kMxChunk * (t + j * TPR), p.K, p.wide);
           g.get(f);
         } else {
           w[j].get(f);
@@ -462,11 +505,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
       float f[kMxChunk];
       if (p.w_f32) {
         MxRaw<float, kVec> g;
-        g.load(static_cast<const float*>(p.weight), kMxChunk * c, p.K);
+        g.load(static_cast<const float*>(p.weight), kMxChunk * c, p.K, p.wide);
         g.get(f);
       } else {
         MxRaw<T, kVec> g;
-        g.load(static_cast<const T*>(p.weight), kMxChunk * c, p.K);
+        g.load(static_cast<const T*>(p.weight), kMxChunk * c, p.K, p.wide);
         g.get(f);
       }
       scaled(c, rstd, f, v);
@@ -522,6 +565,7 @@ struct MxDequantParams {
   const float* row_scale;
   void* out;              // contiguous [M, K]
   int M, K, Kp, KT;
+  int wide;               // as MxRowParams
 };
 
 // value = element * scale (exact in binary32) * row scale, rounded once more to
@@ -561,7 +605,7 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParam
     const float s = FMT == kNvFp4 ? e4m3x2_to_f2(sb).x : e8m0_to_f32(sb);
 #pragma unroll
     for (int e = 0; e < kMxChunk; ++e) v[e] = FMT == kNvFp4 ? v[e] * s * rs : v[e] * s;
-    store_chunk<T, kVec>(out, kMxChunk * c, p.K, v);
+    store_chunk<T, kVec>(out, kMxChunk * c, p.K, p.wide, v);
   }
 }
 

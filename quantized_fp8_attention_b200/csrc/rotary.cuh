@@ -42,41 +42,49 @@ struct RotaryParams {
   uint8_t axis[64];
 };
 
-// A lane's two pieces of four channels of a row, as they lie in memory.
-template <typename T>
+// A lane's channels of a row, two pieces of P, as they lie in memory.
+template <typename T, int P>
 struct RotRaw {
-  uint32_t w[2 * sizeof(T)];
-  template <bool kSplit>
-  __device__ __forceinline__ void load(const T* row, int c0, int c1, bool here) {
+  static constexpr int kWords = P * sizeof(T) / 4;      // of a piece
+  uint32_t w[2 * kWords];
+  __device__ __forceinline__ void piece(const T* p, int at) {
+    if constexpr (kWords % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[i] = 0u;
-    if (!here) return;
-    if constexpr (sizeof(T) == 4) {
-      const uint4 a = *reinterpret_cast<const uint4*>(row + c0), b = *reinterpret_cast<const uint4*>(row + c1);
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-    } else if constexpr (kSplit) {
-      const uint2 a = *reinterpret_cast<const uint2*>(row + c0), b = *reinterpret_cast<const uint2*>(row + c1);
-      w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p + i * 4 / sizeof(T));
+        w[at + i] = a.x; w[at + i + 1] = a.y; w[at + i + 2] = a.z; w[at + i + 3] = a.w;
+      }
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(row + c0);
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      static_assert(kWords == 2, "8 or 16 bytes");
+      const uint2 a = *reinterpret_cast<const uint2*>(p);
+      w[at] = a.x; w[at + 1] = a.y;
     }
   }
-  __device__ __forceinline__ void load_elements(const T* row, int c0, int c1, bool here) {
-    T e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = here ? row[(i < 4 ? c0 : c1 - 4) + i] : from_f32<T>(0.0f);
-#pragma unroll
-    for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[i] = reinterpret_cast<const uint32_t*>(e)[i];
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+  // kJoined: the pieces are neighbours
+  template <bool kJoined>
+  __device__ __forceinline__ void load(const T* row, int c0, int c1, bool vec) {
+    if (vec) {
+      if constexpr (kJoined && kWords == 2) {
+        const uint4 a = *reinterpret_cast<const uint4*>(row + c0);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      } else {
+        piece(row + c0, 0);
+        piece(row + c1, kWords);
+      }
     } else {
+      T e[2 * P];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2 * P; ++i) e[i] = row[i < P ? c0 + i : c1 + i - P];
+#pragma unroll
+      for (int i = 0; i < 2 * kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(e)[i];
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[2 * P]) const {
+#pragma unroll
+    for (int i = 0; i < 2 * kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
         const float2 f = unpack2<T>(w[i]);
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
@@ -85,26 +93,55 @@ struct RotRaw {
   }
 };
 
-// kSplit: pair j is channels (j, pairs + j); otherwise (2j, 2j + 1).  Lane l
-// holds two pieces of four channels: interleaved the neighbours [8l, 8l + 8),
-// split [4l, 4l + 4) and the four partners at pairs + 4l, so that a pair
-// never crosses lanes and each lane forms four angles.
+// kSplit: pair j is channels (j, pairs + j); otherwise (2j, 2j + 1).  Pairs
+// never cross lanes: interleaved a lane of 16 holds eight neighbours (four
+// pairs); split a lane of 8 holds eight channels and their eight partners, and
+// the 16 lanes take two heads at a time.  Every access is 16 bytes a lane (16
+// lanes with 4 + 4 channels, 8 bytes an access, ran at 3.9 instead of 5.8
+// TB/s).  Rows are fetched one batch ahead: the first while the angles are
+// formed, the next while one is rotated.
 template <typename T, bool kSplit>
-__global__ void __launch_bounds__(256, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
-  const int l = threadIdx.x & 15;
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) rotary_kernel(const __grid_constant__ RotaryParams p) {
+  constexpr int LPR = kSplit ? 8 : 16;                 // lanes per row
+  constexpr int P = kSplit ? 8 : 4;                    // channels per piece = pairs per lane
+  constexpr int HS = 16 / LPR;                         // heads at a time
+  constexpr int U = (kSplit ? 2 : 4) / (sizeof(T) == 4 ? 2 : 1);   // batch: U * HS heads
+  const int l = threadIdx.x & (LPR - 1), sub = (threadIdx.x & 15) / LPR;
   const int64_t token = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   const bool here = token < (int64_t)p.B * p.N;
   const int b = here ? (int)(token / p.N) : 0, n = here ? (int)(token - (int64_t)b * p.N) : 0;
   // channels of the lane's two pieces; past the rotated ones, split lanes take
-  // eight plain channels
-  const bool rotates = !kSplit || 4 * l < p.pairs;
-  const int c0 = kSplit && rotates ? 4 * l : 8 * l;
-  const int c1 = kSplit && rotates ? p.pairs + 4 * l : 8 * l + 4;
+  // neighbours
+  const bool rotates = !kSplit || P * l < p.pairs;
+  const int c0 = kSplit && rotates ? P * l : 2 * P * l;
+  const int c1 = kSplit && rotates ? p.pairs + P * l : 2 * P * l + P;
 
-  float cs[4], sn[4];
+  const int total = p.heads[0] + p.heads[1];
+  const int h0 = blockIdx.y * p.heads_per_group, h1 = min(total, h0 + p.heads_per_group);
+  RotRaw<T, P> cur[U];
+  // rows h + sub, h + HS + sub, .. (below `last`) of Q or K
+  auto fetch = [&](int part, int h, int last, RotRaw<T, P> (&raw)[U]) {
+    const T* in = static_cast<const T*>(p.in[part]) + (int64_t)b * p.sb[part] + (int64_t)n * p.sn[part];
+    const int base = part ? p.heads[0] : 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = 4 * l + i;
+    for (int u = 0; u < U; ++u) {
+      const int hh = h + u * HS + sub;
+      if (here && hh < last)
+        raw[u].template load<!kSplit>(in + (int64_t)(hh - base) * p.sh[part], c0, c1, p.vec[part]);
+    }
+  };
+  const int part0 = h0 < p.heads[0] ? 0 : 1;
+  const int last0 = part0 ? h1 : min(h1, p.heads[0]);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < RotRaw<T, P>::kWords * 2; ++i) cur[u].w[i] = 0u;
+  fetch(part0, h0, last0, cur);
+
+  float cs[P], sn[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int j = P * l + i;
     cs[i] = 1.0f;
     sn[i] = 0.0f;
     if (here && j < p.pairs) {
@@ -116,73 +153,65 @@ __global__ void __launch_bounds__(256, 4) rotary_kernel(const __grid_constant__ 
     }
   }
 
-  const int total = p.heads[0] + p.heads[1];
-  const int h0 = blockIdx.y * p.heads_per_group, h1 = min(total, h0 + p.heads_per_group);
-#pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
+  for (int part = part0; part < 2; ++part) {
     const int base = part ? p.heads[0] : 0;
     const int first = max(h0, base), last = min(h1, base + p.heads[part]);
     if (first >= last) continue;
-    float w[8];
+    if (part != part0) fetch(part, first, last, cur);
+    float w[2 * P];
     const bool norm = p.weight[part] != nullptr;
     if (norm) {
       const T* wp = static_cast<const T*>(p.weight[part]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < P; ++e) {
         w[e] = to_f32<T>(wp[c0 + e]);
-        w[4 + e] = to_f32<T>(wp[c1 + e]);
+        w[P + e] = to_f32<T>(wp[c1 + e]);
       }
     }
-    const T* in = static_cast<const T*>(p.in[part]) + (int64_t)b * p.sb[part] + (int64_t)n * p.sn[part];
     T* out = static_cast<T*>(p.out[part]) + ((int64_t)b * p.heads[part] * p.N + n) * kHeadDim;
-    const bool vec = p.vec[part];
-    auto rows = [&](auto count, int h) {
-      constexpr int U = decltype(count)::value;
-      // all loads first, kept as they lie in memory until used
-      RotRaw<T> raw[U];
-      if (vec) {
+    for (int h = first; h < last; h += U * HS) {
+      RotRaw<T, P> next[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u].template load<kSplit>(in + (int64_t)(h + u - base) * p.sh[part], c0, c1, here);
-      } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) raw[u].load_elements(in + (int64_t)(h + u - base) * p.sh[part], c0, c1, here);
-      }
+      for (int u = 0; u < U; ++u) next[u] = cur[u];
+      if (h + U * HS < last) fetch(part, h + U * HS, last, next);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float v[8];
-        raw[u].get(v);
+        const int hh = h + u * HS + sub;
+        float v[2 * P];
+        cur[u].get(v);
         if (norm) {
           float ss = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+          for (int e = 0; e < 2 * P; ++e) ss += v[e] * v[e];
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
           const float r = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
+          for (int e = 0; e < 2 * P; ++e) v[e] = v[e] * r * w[e];
         }
-        float y[8];
+        float y[2 * P];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int a = kSplit ? i : 2 * i, d = kSplit ? 4 + i : 2 * i + 1;
-          const bool on = kSplit ? rotates : 4 * l + i < p.pairs;
+        for (int i = 0; i < P; ++i) {
+          const int a = kSplit ? i : 2 * i, d = kSplit ? P + i : 2 * i + 1;
+          const bool on = kSplit ? rotates : P * l + i < p.pairs;
           y[a] = on ? v[a] * cs[i] - v[d] * sn[i] : v[a];
           y[d] = on ? v[a] * sn[i] + v[d] * cs[i] : v[d];
         }
-        if (here) {
-          T* dst = out + (int64_t)(h + u - base) * p.N * kHeadDim;
-          if constexpr (!kSplit) {
-            store_vec<T, 8>(dst + c0, y);
-          } else {
-            store_vec<T, 4>(dst + c0, {y[0], y[1], y[2], y[3]});
-            store_vec<T, 4>(dst + c1, {y[4], y[5], y[6], y[7]});
+        if (here && hh < last) {
+          T* dst = out + (int64_t)(hh - base) * p.N * kHeadDim;
+          uint32_t q[RotRaw<T, P>::kWords * 2];
+          pack_words<T, 2 * P>(y, q);
+          constexpr int W = RotRaw<T, P>::kWords;
+#pragma unroll
+          for (int i = 0; i < 2 * W; i += 4) {         // (a 16-byte store may span two neighbouring pieces)
+            T* at = dst + (i < W ? c0 : c1 - P) + i * 4 / (int)sizeof(T);
+            *reinterpret_cast<uint4*>(at) = make_uint4(q[i], q[i + 1], q[i + 2], q[i + 3]);
           }
         }
       }
-    };
-    int h = first;
-    for (; h + 4 <= last; h += 4) rows(std::integral_constant<int, 4>{}, h);
-    for (; h < last; ++h) rows(std::integral_constant<int, 1>{}, h);
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u] = next[u];
+    }
   }
 }
 
