@@ -247,22 +247,24 @@ static size_t dtype_bytes(int t) { return t == FQA_DTYPE_F32 ? 4 : 2; }
 // -------------------------------------------- launches of microscaled rows
 
 // One launch of the row kernel that fits the row: 16 elements a thread and
-// chunk, two chunks in registers.  Threads per row by its length: a warp up to
-// 1024 elements (no block-wide sums), then 128, 256 and 512 up to 16384; longer
-// rows, and rows off the 16-byte boundaries, are read again for each step.
+// chunk, two chunks in registers (one of binary32: 103 registers a thread left
+// two CTAs per SM, 23 us for 1023 x 5100).  Threads per row by its length: a
+// warp for short ones (no block-wide sums), then 128, 256 and 512; longer rows,
+// and rows off the 16-byte boundaries, are read again for each step.
 template <typename T, int FMT, bool kNorm>
 static void launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s) {
-  const int width = p.KT * MxTraits<FMT>::kWordChunks * kMxChunk;
+  constexpr int NCH = sizeof(T) == 4 ? 1 : 2;
+  const int threads = p.KT * MxTraits<FMT>::kWordChunks / NCH;   // that hold the row's words, whole
   if (!vec)
     mx_row_kernel<T, FMT, kNorm, 128, 1, true, false><<<p.M, 128, 0, s>>>(p);
-  else if (width <= 1024)
-    mx_row_kernel<T, FMT, kNorm, 32, 2, false, true><<<(p.M + 3) / 4, 128, 0, s>>>(p);
-  else if (width <= 4096)
-    mx_row_kernel<T, FMT, kNorm, 128, 2, false, true><<<p.M, 128, 0, s>>>(p);
-  else if (width <= 8192)
-    mx_row_kernel<T, FMT, kNorm, 256, 2, false, true><<<p.M, 256, 0, s>>>(p);
-  else if (width <= 16384)
-    mx_row_kernel<T, FMT, kNorm, 512, 2, false, true><<<p.M, 512, 0, s>>>(p);
+  else if (threads <= 32)
+    mx_row_kernel<T, FMT, kNorm, 32, NCH, false, true><<<(p.M + 3) / 4, 128, 0, s>>>(p);
+  else if (threads <= 128)
+    mx_row_kernel<T, FMT, kNorm, 128, NCH, false, true><<<p.M, 128, 0, s>>>(p);
+  else if (threads <= 256)
+    mx_row_kernel<T, FMT, kNorm, 256, NCH, false, true><<<p.M, 256, 0, s>>>(p);
+  else if (threads <= 512)
+    mx_row_kernel<T, FMT, kNorm, 512, NCH, false, true><<<p.M, 512, 0, s>>>(p);
   else
     mx_row_kernel<T, FMT, kNorm, 512, 1, true, true><<<p.M, 512, 0, s>>>(p);
 }
@@ -317,10 +319,10 @@ static fqa_status launch_mx_small(const uint8_t* a, const uint8_t* b, const MxMa
   CUtensorMap tp, tq;
   if (!make_tmap_rows(&tp, b, row_bytes, p.N, 128) || !make_tmap_rows(&tq, a, row_bytes, p.M, NT)) return FQA_ERR_CUDA;
   const int64_t tiles = (int64_t)((p.N + 127) / 128) * ((p.M + NT - 1) / NT);
-  // split K while the CTAs stay within two per SM and each keeps two stages
+  // split K while all CTAs are resident at once and each keeps two stages
   const int stages = (p.mmas + 3) / 4;
   int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= 2 * num_sms() && stages >= 4 * ranks) ranks *= 2;
+  while (ranks < 8 && tiles * ranks * 2 <= T::kPerSm * num_sms() && stages >= 4 * ranks) ranks *= 2;
   if (tiles * ranks > INT32_MAX) return FQA_ERR_UNSUPPORTED;
   const auto fn = mx_matmul_small_kernel<FMT, NT>;
   if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess)
@@ -378,6 +380,10 @@ static fqa_status launch_mx_matmul(const uint8_t* a, const uint8_t* b, const MxM
   if (p.M <= 16) return launch_mx_small<FMT, 16>(a, b, p, row_bytes, s);
   if (p.M <= 32) return launch_mx_small<FMT, 32>(a, b, p, row_bytes, s);
   if (p.M <= 64) return launch_mx_small<FMT, 64>(a, b, p, row_bytes, s);
+#ifdef MX_LARGE_FROM
+  if (p.M < MX_LARGE_FROM) return launch_mx_small<FMT, 128>(a, b, p, row_bytes, s);
+  return launch_mx_large<FMT>(a, b, p, row_bytes, s);
+#endif
   if (p.M <= 128) return launch_mx_small<FMT, 128>(a, b, p, row_bytes, s);
   return launch_mx_large<FMT>(a, b, p, row_bytes, s);
 }

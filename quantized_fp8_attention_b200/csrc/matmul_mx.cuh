@@ -18,8 +18,6 @@
 // results, so the scale tiles' rows past the end need no value.
 #pragma once
 
-#include <cooperative_groups.h>
-
 #include "attention.cuh"
 #include "device.cuh"
 #include "microscale.cuh"
@@ -86,6 +84,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
 }
 
+// Shared address of the same offset in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+// Barrier of all threads of the cluster, in two halves (whole warps).
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 struct MxMatmulParams {
   const uint8_t* sa;      // scale tiles of A [M] and B [N]
   const uint8_t* sb;
@@ -116,8 +133,10 @@ __device__ __forceinline__ void store_out(void* out, int type, size_t at, float 
 // handful of tokens costs an MMA of N = 16, not one of 128 padded rows, and
 // the kernel is bound by the weights' bytes.  The CTAs of a cluster split K:
 // at 4096 features there are 32 tiles of weights for 148 SMs, so the stages
-// are dealt out to `ranks` CTAs and their binary32 partial tiles are added in
-// rank order over distributed shared memory (the same sum every time).
+// are dealt out to `ranks` CTAs.  Token q of the tile belongs to rank q % ranks;
+// every CTA writes its binary32 partial sums into the owner's shared memory,
+// and after one cluster barrier the owner adds them in rank order (the same sum
+// every time).
 //   warp 0  TMA producer    warp 1  TMEM owner and MMA issuer
 //   warps 2-5  epilogue, one lane quarter each
 constexpr int kMxSmallThreads = 192;
@@ -127,15 +146,16 @@ struct MxSmall {
   using Mma = MxMma<FMT>;
   static constexpr int kPBytes = 128 * 128, kQBytes = NT * 128, kSfBytes = 512 * Mma::kWords;
   static constexpr int kStageBytes = kPBytes + (kQBytes < 1024 ? 1024 : kQBytes) + 2 * kSfBytes;
-  static constexpr int kStages = 4;
-  static constexpr int kOffBar = kStages * kStageBytes;
+  static constexpr int kStages = NT == 32 ? 3 : 4;           // (32: two CTAs still fit an SM)
+  static constexpr int kOffPart = kStages * kStageBytes;     // partial sums of this rank's rows: [rank][NT / ranks][128]
+  static constexpr int kOffBar = kOffPart + NT * 128 * 4;
   static constexpr int kSmemBytes = kOffBar + (2 * kStages + 1) * 8 + 16 + 1024;
   static constexpr int kSfCols = 8 * Mma::kWords;            // per stage: four for P and four for Q, per word
   static constexpr int kColSf = NT < 32 ? 32 : NT;
   static constexpr int kColsUsed = kColSf + kStages * kSfCols;
   static constexpr int kCols = kColsUsed <= 64 ? 64 : (kColsUsed <= 128 ? 128 : 256);
-  static_assert(kColsUsed <= 256 && kStageBytes % 1024 == 0, "tile layout");
-  static_assert(NT * 128 * 4 <= kStages * kStageBytes, "a partial tile fits the stages");
+  static constexpr int kPerSm = 2 * (kSmemBytes + 1024) <= 228 * 1024 ? 2 : 1;
+  static_assert(kColsUsed <= 256 && kStageBytes % 1024 == 0 && kSmemBytes <= 232448, "tile layout");
 };
 
 template <int FMT, int NT>
@@ -160,6 +180,17 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   // this rank's stages: [s0, s1), an even share
   const int s0 = (int)((int64_t)stages * rank / ranks), s1 = (int)((int64_t)stages * (rank + 1) / ranks);
 
+  auto load_stage = [&](int s, int slot) {         // one thread
+    uint8_t* st = smem + slot * T::kStageBytes;
+    const uint32_t words = min((int)Mma::kWords, p.KT - s * (int)Mma::kWords);
+    mbar_arrive_expect_tx(&full[slot], T::kPBytes + T::kQBytes + 2 * 512 * words);
+    tma_load_2d(st, &tmP, &full[slot], s * 128, p0);
+    tma_load_2d(st + T::kPBytes, &tmQ, &full[slot], s * 128, q0);
+    uint8_t* sf = st + T::kStageBytes - 2 * T::kSfBytes;
+    const size_t w0 = (size_t)s * Mma::kWords * 512;
+    bulk_load_plain(sf, p.sb + (size_t)(p0 / 128) * p.KT * 512 + w0, 512 * words, &full[slot]);
+    bulk_load_plain(sf + T::kSfBytes, p.sa + (size_t)(q0 / 128) * p.KT * 512 + w0, 512 * words, &full[slot]);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -168,34 +199,28 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     mbar_init(done, 1);
     *abort_flag = 0;
     mbar_fence_init();
+    // the ring's first fill needs nothing else of the CTA
+    for (int s = s0; s < min(s1, s0 + T::kStages); ++s) load_stage(s, s - s0);
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc(tmem_slot, T::kCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
+  if (ranks > 1) cluster_arrive();   // waited for before the first access to a peer
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   // (both issuing warps stay whole and elect a lane per step: see the issuer of
   // the large kernel)
   if (warp == 0) {
-    int issued = 0;
-    for (int s = s0; s < s1; ++s) {
+    int issued = min(s1 - s0, T::kStages);
+    for (int s = s0 + issued; s < s1; ++s) {
       const int i = s - s0, slot = i % T::kStages;
       if (!warp_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status)) break;
-      if (elect_one()) {
-        uint8_t* st = smem + slot * T::kStageBytes;
-        const uint32_t words = min((int)Mma::kWords, p.KT - s * (int)Mma::kWords);
-        mbar_arrive_expect_tx(&full[slot], T::kPBytes + T::kQBytes + 2 * 512 * words);
-        tma_load_2d(st, &tmP, &full[slot], s * 128, p0);
-        tma_load_2d(st + T::kPBytes, &tmQ, &full[slot], s * 128, q0);
-        uint8_t* sf = st + T::kStageBytes - 2 * T::kSfBytes;
-        const size_t w0 = (size_t)s * Mma::kWords * 512;
-        bulk_load_plain(sf, p.sb + (size_t)(p0 / 128) * p.KT * 512 + w0, 512 * words, &full[slot]);
-        bulk_load_plain(sf + T::kSfBytes, p.sa + (size_t)(q0 / 128) * p.KT * 512 + w0, 512 * words, &full[slot]);
-      }
+      if (elect_one()) load_stage(s, slot);
       __syncwarp();
       issued = i + 1;
     }
@@ -246,46 +271,72 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
   const int pr = p0 + row;
   const int nq = min(NT, p.M - q0);                          // rows of A in the tile
-  const float rb = (p.rb != nullptr && pr < p.N) ? p.rb[pr] : 1.0f;
-  const float bias = (p.bias != nullptr && pr < p.N) ? p.bias[pr] : 0.0f;
-  auto finish = [&](float acc, int qi) {
-    if (pr >= p.N) return;
-    const float ra = p.ra != nullptr ? __ldg(p.ra + q0 + qi) : 1.0f;
-    store_out(p.out, p.out_type, (size_t)(q0 + qi) * p.N + pr, p.ra != nullptr ? fmaf(acc * ra, rb, bias) : acc + bias);
-  };
-  float* part = reinterpret_cast<float*>(smem);              // [NT][128], over the drained stages
+  const bool scaled = p.ra != nullptr;
+  float rb = 1.0f, bias = 0.0f;
+  float ra[(NT + 31) / 32];                                  // of token 32 j + lane, handed out by shuffles
   if (warp >= 2) {
-    const bool ok = warp_wait(done, 0, abort_flag, p.status);
-    tc_fence_after();
-    if (ok) {
-#pragma unroll 1
-      for (int c = 0; c < NT; c += 16) {
-        uint32_t u[16];
-        tmem_ld16(tmem + lane_off + (uint32_t)c, u);
-        tmem_wait_ld();
+    // (fetched while the products run: one load per use held each token up by a
+    // memory latency)
+    if (pr < p.N) {
+      if (p.rb != nullptr) rb = p.rb[pr];
+      if (p.bias != nullptr) bias = p.bias[pr];
+    }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float acc = s1 > s0 ? __uint_as_float(u[e]) : 0.0f;
-          if (ranks > 1)
-            part[(c + e) * 128 + row] = acc;
-          else if (c + e < nq)
-            finish(acc, c + e);
+    for (int j = 0; j < (NT + 31) / 32; ++j) {
+      const int q = 32 * j + lane;
+      ra[j] = scaled && q < nq ? p.ra[q0 + q] : 1.0f;
+    }
+  }
+  auto token_scale = [&](int q) {                            // q the same in all lanes
+    float v = ra[0];
+#pragma unroll
+    for (int j = 1; j < (NT + 31) / 32; ++j) v = (q >> 5) == j ? ra[j] : v;
+    return __shfl_sync(0xFFFFFFFFu, v, q & 31);
+  };
+  auto finish = [&](float acc, int q, float r) {
+    if (q < nq && pr < p.N)
+      store_out(p.out, p.out_type, (size_t)(q0 + q) * p.N + pr, scaled ? fmaf(acc * r, rb, bias) : acc + bias);
+  };
+  bool ok = true;
+  if (warp >= 2) {
+    ok = warp_wait(done, 0, abort_flag, p.status);
+    tc_fence_after();
+  }
+  if (ranks > 1) cluster_wait();
+  const int lg = 31 - __clz(ranks);                          // ranks: a power of two
+  float* part = reinterpret_cast<float*>(smem + T::kOffPart);
+  if (warp >= 2 && ok) {
+    const uint32_t mine = smem_u32(part) + 4u * (uint32_t)(rank * (NT >> lg) * 128 + row);
+#pragma unroll 1
+    for (int c = 0; c < nq; c += 16) {
+      uint32_t u[16];
+      tmem_ld16(tmem + lane_off + (uint32_t)c, u);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int q = c + e;
+        if (ranks == 1) {
+          finish(__uint_as_float(u[e]), q, scaled ? token_scale(q) : 1.0f);
+        } else if (q < nq) {
+          st_cluster(mapa_u32(mine + 512u * (uint32_t)(q >> lg), (uint32_t)(q & (ranks - 1))), u[e]);
         }
       }
     }
     tc_fence_before();
   }
   if (ranks > 1) {
-    namespace cg = cooperative_groups;
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
+    cluster_arrive();
+    cluster_wait();
     if (warp >= 2)
-      for (int qi = rank; qi < nq; qi += ranks) {
-        float acc = 0.0f;
-        for (int r = 0; r < ranks; ++r) acc += cluster.map_shared_rank(part, r)[qi * 128 + row];
-        finish(acc, qi);
+      for (int q = rank; q < nq; q += ranks) {
+        const float* at = part + (q >> lg) * 128 + row;
+        float v[8], acc = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = r < ranks ? at[r * (NT >> lg) * 128] : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) acc += v[r];
+        finish(acc, q, scaled ? token_scale(q) : 1.0f);
       }
-    cluster.sync();          // nobody leaves while its partial tile may be read
   }
   __syncthreads();
   if (warp == 1) {
@@ -332,12 +383,6 @@ struct MxLarge {
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
-// Shared address of the same offset in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 // Arrival on a barrier of the cluster.  Only tensor memory is handed over with
 // it (ordered by the tcgen05 fences around), so the order of ordinary memory
 // stays within the CTA: a release to the cluster waits for every outstanding
@@ -380,10 +425,6 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
           smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -439,7 +480,8 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();                // the peer's barriers are ready too
+  cluster_arrive();
+  cluster_wait();                // the peer's barriers are ready too
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -649,7 +691,8 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  cluster_arrive();
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
