@@ -319,10 +319,14 @@ static fqa_status launch_mx_small(const uint8_t* a, const uint8_t* b, const MxMa
   CUtensorMap tp, tq;
   if (!make_tmap_rows(&tp, b, row_bytes, p.N, 128) || !make_tmap_rows(&tq, a, row_bytes, p.M, NT)) return FQA_ERR_CUDA;
   const int64_t tiles = (int64_t)((p.N + 127) / 128) * ((p.M + NT - 1) / NT);
-  // split K while all CTAs are resident at once and each keeps two stages
-  const int stages = (p.mmas + 3) / 4;
+  // split K while all CTAs are resident at once and each keeps two stages; a
+  // cluster of eight wants that many free SMs in one GPC, so only up to three
+  // quarters of the places (32 tiles: 5.5 us in fours, 6.7 in eights; 8 tiles:
+  // 5.7 and 4.9; 16 tiles with one CTA per SM: 8.2 and 12.0)
+  const int stages = (p.mmas + 3) / 4, places = T::kPerSm * num_sms();
   int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= T::kPerSm * num_sms() && stages >= 4 * ranks) ranks *= 2;
+  while (ranks < T::kMaxRanks && tiles * ranks * 2 <= (ranks == 4 ? places * 3 / 4 : places) && stages >= 4 * ranks)
+    ranks *= 2;
   if (tiles * ranks > INT32_MAX) return FQA_ERR_UNSUPPORTED;
   const auto fn = mx_matmul_small_kernel<FMT, NT>;
   if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess)
@@ -374,17 +378,18 @@ static fqa_status launch_mx_large(const uint8_t* a, const uint8_t* b, const MxMa
   return launch_status();
 }
 
+// The kernel by the product's size: the narrowest tile of tokens that holds
+// them all, up to 128 x 128 tiles while one round of SMs holds those; beyond,
+// pairs on 256 x 256 tiles.  At K = 4096, N = 4096 (nvfp4): 512 rows, 128
+// tiles, 11.4 us against 12.1; 768 rows, 192 tiles, 21.4 against 12.6.
 template <int FMT>
 static fqa_status launch_mx_matmul(const uint8_t* a, const uint8_t* b, const MxMatmulParams& p, int row_bytes,
                                    cudaStream_t s) {
   if (p.M <= 16) return launch_mx_small<FMT, 16>(a, b, p, row_bytes, s);
   if (p.M <= 32) return launch_mx_small<FMT, 32>(a, b, p, row_bytes, s);
   if (p.M <= 64) return launch_mx_small<FMT, 64>(a, b, p, row_bytes, s);
-#ifdef MX_LARGE_FROM
-  if (p.M < MX_LARGE_FROM) return launch_mx_small<FMT, 128>(a, b, p, row_bytes, s);
-  return launch_mx_large<FMT>(a, b, p, row_bytes, s);
-#endif
-  if (p.M <= 128) return launch_mx_small<FMT, 128>(a, b, p, row_bytes, s);
+  const int64_t tiles = (int64_t)((p.M + 127) / 128) * ((p.N + 127) / 128);
+  if (tiles <= num_sms()) return launch_mx_small<FMT, 128>(a, b, p, row_bytes, s);
   return launch_mx_large<FMT>(a, b, p, row_bytes, s);
 }
 

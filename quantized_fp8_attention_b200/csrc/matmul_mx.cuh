@@ -18,6 +18,8 @@
 // results, so the scale tiles' rows past the end need no value.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.cuh"
 #include "device.cuh"
 #include "microscale.cuh"
@@ -90,8 +92,19 @@ __device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // Barrier of all threads of the cluster, in two halves (whole warps).
 __device__ __forceinline__ void cluster_arrive() {
@@ -117,15 +130,6 @@ struct MxMatmulParams {
   uint32_t* status;
 };
 
-__device__ __forceinline__ void store_out(void* out, int type, size_t at, float v) {
-  if (type == 0)
-    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
-  else if (type == 1)
-    static_cast<float*>(out)[at] = v;
-  else
-    static_cast<__half*>(out)[at] = __float2half_rn(v);
-}
-
 // ------------------------------------------------------- few rows of A
 //
 // One 128 x NT tile per cluster of 1, 2, 4 or 8 CTAs.  B's rows (the weights)
@@ -133,22 +137,28 @@ __device__ __forceinline__ void store_out(void* out, int type, size_t at, float 
 // handful of tokens costs an MMA of N = 16, not one of 128 padded rows, and
 // the kernel is bound by the weights' bytes.  The CTAs of a cluster split K:
 // at 4096 features there are 32 tiles of weights for 148 SMs, so the stages
-// are dealt out to `ranks` CTAs.  Token q of the tile belongs to rank q % ranks;
-// every CTA writes its binary32 partial sums into the owner's shared memory,
-// and after one cluster barrier the owner adds them in rank order (the same sum
-// every time).
+// are dealt out to `ranks` CTAs.  Group g of four tokens belongs to rank
+// g % ranks; every CTA writes its binary32 partial sums into the owner's shared
+// memory, 16 bytes a thread, and after one cluster barrier the owner adds them
+// in rank order (the same sum every time).
 //   warp 0  TMA producer    warp 1  TMEM owner and MMA issuer
-//   warps 2-5  epilogue, one lane quarter each
-constexpr int kMxSmallThreads = 192;
+//   warps 2-9  epilogue: lane quarter warp % 4, every other group of tokens
+// (One warp per scheduler runs the epilogue, so its time is its instruction
+// count: token by token it took 100 cycles to push and 400 to add up each.)
+constexpr int kMxSmallThreads = 320;
 
 template <int FMT, int NT>
 struct MxSmall {
   using Mma = MxMma<FMT>;
+  static constexpr int kMaxRanks = 8;
   static constexpr int kPBytes = 128 * 128, kQBytes = NT * 128, kSfBytes = 512 * Mma::kWords;
   static constexpr int kStageBytes = kPBytes + (kQBytes < 1024 ? 1024 : kQBytes) + 2 * kSfBytes;
   static constexpr int kStages = NT == 32 ? 3 : 4;           // (32: two CTAs still fit an SM)
-  static constexpr int kOffPart = kStages * kStageBytes;     // partial sums of this rank's rows: [rank][NT / ranks][128]
-  static constexpr int kOffBar = kOffPart + NT * 128 * 4;
+  static constexpr int kOffPart = kStages * kStageBytes;     // partial sums of this rank's groups: [group / ranks][source][128] x 4
+  // slots of 128 threads x 16 bytes: one per group, and at least one per rank
+  static constexpr int kPartBytes = (NT / 4 < kMaxRanks ? kMaxRanks : NT / 4) * 2048;
+  static constexpr int kOffRa = kOffPart + kPartBytes;       // row scales of the tile's tokens
+  static constexpr int kOffBar = kOffRa + NT * 4;
   static constexpr int kSmemBytes = kOffBar + (2 * kStages + 1) * 8 + 16 + 1024;
   static constexpr int kSfCols = 8 * Mma::kWords;            // per stage: four for P and four for Q, per word
   static constexpr int kColSf = NT < 32 ? 32 : NT;
@@ -268,34 +278,43 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   }
   // ------------------------------------------------ epilogue
   const int row = 32 * (warp & 3) + lane;                   // of P: an output feature
-  const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+  const int half = (warp - 2) >> 2;
   const int pr = p0 + row;
   const int nq = min(NT, p.M - q0);                          // rows of A in the tile
   const bool scaled = p.ra != nullptr;
   float rb = 1.0f, bias = 0.0f;
-  float ra[(NT + 31) / 32];                                  // of token 32 j + lane, handed out by shuffles
+  float* ra = reinterpret_cast<float*>(smem + T::kOffRa);
   if (warp >= 2) {
-    // (fetched while the products run: one load per use held each token up by a
-    // memory latency)
+    // fetched while the products run
+    const int q = threadIdx.x - 64;
+    if (q < NT) ra[q] = scaled && q < nq ? p.ra[q0 + q] : 1.0f;
     if (pr < p.N) {
       if (p.rb != nullptr) rb = p.rb[pr];
       if (p.bias != nullptr) bias = p.bias[pr];
     }
-#pragma unroll
-    for (int j = 0; j < (NT + 31) / 32; ++j) {
-      const int q = 32 * j + lane;
-      ra[j] = scaled && q < nq ? p.ra[q0 + q] : 1.0f;
-    }
+    bar_sync(1, kMxSmallThreads - 64);
   }
-  auto token_scale = [&](int q) {                            // q the same in all lanes
-    float v = ra[0];
+  // tokens q .. q + 3 of this thread's feature
+  auto finish = [&](const float (&acc)[4], int q) {
+    if (pr >= p.N) return;
+    const float4 r = *reinterpret_cast<const float4*>(ra + q);
+    const float v[4] = {scaled ? fmaf(acc[0] * r.x, rb, bias) : acc[0] + bias,
+                        scaled ? fmaf(acc[1] * r.y, rb, bias) : acc[1] + bias,
+                        scaled ? fmaf(acc[2] * r.z, rb, bias) : acc[2] + bias,
+                        scaled ? fmaf(acc[3] * r.w, rb, bias) : acc[3] + bias};
+    const size_t at = (size_t)(q0 + q) * p.N + pr;
+    auto store = [&](auto* out) {
+      using O = std::remove_pointer_t<decltype(out)>;
 #pragma unroll
-    for (int j = 1; j < (NT + 31) / 32; ++j) v = (q >> 5) == j ? ra[j] : v;
-    return __shfl_sync(0xFFFFFFFFu, v, q & 31);
-  };
-  auto finish = [&](float acc, int q, float r) {
-    if (q < nq && pr < p.N)
-      store_out(p.out, p.out_type, (size_t)(q0 + q) * p.N + pr, scaled ? fmaf(acc * r, rb, bias) : acc + bias);
+      for (int e = 0; e < 4; ++e)
+        if (q + e < nq) out[at + (size_t)e * p.N] = from_f32<O>(v[e]);
+    };
+    if (p.out_type == 0)
+      store(static_cast<__nv_bfloat16*>(p.out));
+    else if (p.out_type == 1)
+      store(static_cast<float*>(p.out));
+    else
+      store(static_cast<__half*>(p.out));
   };
   bool ok = true;
   if (warp >= 2) {
@@ -304,21 +323,24 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   }
   if (ranks > 1) cluster_wait();
   const int lg = 31 - __clz(ranks);                          // ranks: a power of two
-  float* part = reinterpret_cast<float*>(smem + T::kOffPart);
+  const uint32_t part = smem_u32(smem + T::kOffPart) + 16u * (uint32_t)row;
   if (warp >= 2 && ok) {
-    const uint32_t mine = smem_u32(part) + 4u * (uint32_t)(rank * (NT >> lg) * 128 + row);
+    const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll 1
-    for (int c = 0; c < nq; c += 16) {
+    for (int c = 16 * half; c < nq; c += 32) {
       uint32_t u[16];
-      tmem_ld16(tmem + lane_off + (uint32_t)c, u);
+      tmem_ld16(acc + (uint32_t)c, u);
       tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int q = c + e;
+      for (int e = 0; e < 16; e += 4) {
+        if (c + e >= nq) break;
         if (ranks == 1) {
-          finish(__uint_as_float(u[e]), q, scaled ? token_scale(q) : 1.0f);
-        } else if (q < nq) {
-          st_cluster(mapa_u32(mine + 512u * (uint32_t)(q >> lg), (uint32_t)(q & (ranks - 1))), u[e]);
+          finish({__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])},
+                 c + e);
+        } else {
+          const int g = (c + e) >> 2;
+          st_cluster_v4(mapa_u32(part + 2048u * (uint32_t)(((g >> lg) << lg) + rank), (uint32_t)(g & (ranks - 1))),
+                        &u[e]);
         }
       }
     }
@@ -328,14 +350,18 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     cluster_arrive();
     cluster_wait();
     if (warp >= 2)
-      for (int q = rank; q < nq; q += ranks) {
-        const float* at = part + (q >> lg) * 128 + row;
-        float v[8], acc = 0.0f;
+      for (int i = half; 4 * ((i << lg) + rank) < nq; i += 2) {
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t v[T::kMaxRanks][4];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = r < ranks ? at[r * (NT >> lg) * 128] : 0.0f;
+        for (int r = 0; r < T::kMaxRanks; ++r)
+          if (r < ranks) ld_shared_v4(part + 2048u * (uint32_t)((i << lg) + r), v[r]);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) acc += v[r];
-        finish(acc, q, scaled ? token_scale(q) : 1.0f);
+        for (int r = 0; r < T::kMaxRanks; ++r)
+          if (r < ranks)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] += __uint_as_float(v[r][e]);
+        finish(acc, 4 * ((i << lg) + rank));
       }
   }
   __syncthreads();
@@ -426,10 +452,6 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // Tile t of mt x nt: bands of eight row tiles, column by column within a
 // band, so that the pairs at work share A's and B's tiles in L2.
 __device__ __forceinline__ void large_tile(int64_t t, int mt, int nt, int& m, int& n) {
@@ -631,22 +653,27 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
           }
         } else {
           __syncwarp();
-          const int rows = min(32, p.M - row0);
-          for (int r = 0; r < rows; ++r) {
-            for (int j = lane; j < width; j += 32) {
-              const int n = n0 + col0 + j;
-              if (n >= p.N) continue;
-              const size_t at = (size_t)(row0 + r) * p.N + n;
-              const uint32_t b = (uint32_t)j * (128u / (uint32_t)width);
-              const uint32_t addr = stage + (uint32_t)r * 128u + (((b >> 4) ^ (uint32_t)(r & 7)) << 4) + (b & 15u);
-              if (width == 32) {
-                uint32_t v;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-                static_cast<uint32_t*>(p.out)[at] = v;
-              } else {
-                uint16_t v;
-                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr));
-                static_cast<uint16_t*>(p.out)[at] = v;
+          // lanes side by side along the row; eight rows' values before their stores
+          const uint32_t per = 128u / (uint32_t)width;       // bytes per value
+          for (int j = lane; j < width; j += 32) {
+            const int n = n0 + col0 + j;
+            const uint32_t byte = (uint32_t)j * per;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+              uint32_t v[8];
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {                  // (row r0 + r of the stage: its chunks are swizzled by r)
+                const uint32_t at = stage + (uint32_t)(r0 + r) * 128u + (((byte >> 4) ^ (uint32_t)r) << 4) + (byte & 12u);
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[r]) : "r"(at));
+              }
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                if (n >= p.N || row0 + r0 + r >= p.M) continue;
+                const size_t at = (size_t)(row0 + r0 + r) * p.N + n;
+                if (width == 32)
+                  static_cast<uint32_t*>(p.out)[at] = v[r];
+                else
+                  static_cast<uint16_t*>(p.out)[at] = (uint16_t)(v[r] >> (8u * (byte & 2u)));
               }
             }
           }
