@@ -268,15 +268,44 @@ __device__ __forceinline__ int power_byte(uint32_t amax, int top, uint32_t part,
 // 2^(127 - byte) for 0 <= byte <= 253.
 __device__ __forceinline__ float inverse_power(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 
+// Eight binary32 values -> eight E2M1 codes in one word, v[0] in bits [0,4).
 __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
-  return e2m1x2(v[0], v[1]) | (e2m1x2(v[2], v[3]) << 8) | (e2m1x2(v[4], v[5]) << 16) | (e2m1x2(v[6], v[7]) << 24);
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// v * s and fma(v, a, v * b) for a chunk, two values an instruction.
+__device__ __forceinline__ void chunk_mul(float (&v)[kMxChunk], float s) {
+#pragma unroll
+  for (int e = 0; e < kMxChunk; e += 2) {
+    const float2 r = f2_mul(make_float2(v[e], v[e + 1]), make_float2(s, s));
+    v[e] = r.x;
+    v[e + 1] = r.y;
+  }
+}
+__device__ __forceinline__ void chunk_mul2(float (&v)[kMxChunk], float a, float b) {
+#pragma unroll
+  for (int e = 0; e < kMxChunk; e += 2) {
+    const float2 x = make_float2(v[e], v[e + 1]);
+    const float2 r = f2_fma(x, make_float2(a, a), f2_mul(x, make_float2(b, b)));
+    v[e] = r.x;
+    v[e + 1] = r.y;
+  }
 }
 
 struct MxRowParams {
   const void* x;          // [M] rows of K, row stride ldx (elements)
   const void* residual;   // the same shape, row stride ldr; binary32 if res_f32, else x's type
   void* residual_out;     // contiguous [M,K], residual's type
-  const void* weight;     // [K], binary32 if w_f32, else x's type
+  const void* weight;     // [K], binary32 if w_f32, else x's type (so w_f32 and res_f32 are 0 for binary32 x)
   int64_t ldx, ldr;
   float eps;
   int M, K, Kp, KT;       // KT words of four scales per row
@@ -288,48 +317,43 @@ struct MxRowParams {
 };
 
 // Writes chunk c (elements [16c, 16c + 16)) of a row whose codes and scale
-// words start at `codes` and `words`.  Called by whole warps with consecutive
-// c, so the threads of a scale and of a word are neighbours.  row_amax: the
-// row's largest magnitude (nvfp4).
+// words start at `codes` and `words`; amax: the chunk's largest magnitude,
+// row_amax: the row's (nvfp4).  Called by whole warps with consecutive c, so the
+// threads of a scale and of a word are neighbours.
 template <int FMT>
 __device__ __forceinline__ void emit_chunk(const MxRowParams& p, uint8_t* codes, uint32_t* words, int c,
-                                           float (&v)[kMxChunk], uint32_t row_amax) {
+                                           float (&v)[kMxChunk], uint32_t amax, uint32_t row_amax) {
   using F = MxTraits<FMT>;
-  uint32_t amax = chunk_amax(v);
 #pragma unroll
   for (int o = 1; o < F::kBlockChunks; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
   uint32_t byte = 0;
+  bool zero = false;
   if constexpr (FMT == kNvFp4) {
-    float hi = 0.0f, lo = 0.0f, inv = 0.0f;
     if (row_amax < 0x7F800000u) {
-      inv = inverse_power(power_byte(row_amax, 11, 0x280000u, 1));
+      const int e = power_byte(row_amax, 11, 0x280000u, 1);
+      const float inv = inverse_power(e);
       byte = e4m3x2(__fdiv_rn(__uint_as_float(amax) * inv, 6.0f), 0.0f) & 0xFFu;
-    }
-    if (byte != 0) {
       const float s = e4m3x2_to_f2(byte).x;
-      hi = __frcp_rz(s);               // rounded down: lo >= 0, so a zero keeps its sign below
-      lo = __fmul_rn(__fmaf_rn(-s, hi, 1.0f), hi);
-#pragma unroll
-      for (int e = 0; e < kMxChunk; ++e) {
-        const float y = __fmul_rn(v[e], inv);
-        v[e] = __fmaf_rn(y, hi, __fmul_rn(y, lo));
+      float hi = __frcp_rz(s);         // rounded down: lo >= 0, so a zero keeps its sign below
+      float lo = __fmul_rn(__fmaf_rn(-s, hi, 1.0f), hi);
+      if (e >= 27 && e <= 207) {       // the row's power goes into both parts, exactly
+        hi *= inv;
+        lo *= inv;
+      } else {                         // where they would leave binary32, into the values
+        chunk_mul(v, inv);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kMxChunk; ++e) v[e] = 0.0f;
+      if (byte != 0) chunk_mul2(v, hi, lo);
     }
+    zero = byte == 0;
   } else {
-    const bool finite = amax < 0x7F800000u;
-    byte = finite ? (uint32_t)(FMT == kMxFp8 ? power_byte(amax, 8, 0x600000u, 0) : power_byte(amax, 2, 0x400000u, 0))
-                  : 0xFFu;
-    if (finite) {
-      const float inv = inverse_power((int)byte);
+    zero = amax >= 0x7F800000u;
+    byte = zero ? 0xFFu
+                : (uint32_t)(FMT == kMxFp8 ? power_byte(amax, 8, 0x600000u, 0) : power_byte(amax, 2, 0x400000u, 0));
+    if (!zero) chunk_mul(v, inverse_power((int)byte));
+  }
+  if (zero) {
 #pragma unroll
-      for (int e = 0; e < kMxChunk; ++e) v[e] = __fmul_rn(v[e], inv);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kMxChunk; ++e) v[e] = 0.0f;
-    }
+    for (int e = 0; e < kMxChunk; ++e) v[e] = 0.0f;
   }
   if (kMxChunk * c < p.Kp) {
     if constexpr (FMT == kMxFp8)
@@ -397,7 +421,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
     float r[kMxChunk];
     raw.get(r);
 #pragma unroll
-    for (int e = 0; e < kMxChunk; ++e) v[e] = __fadd_rn(v[e], r[e]);
+    for (int e = 0; e < kMxChunk; e += 2) {
+      const float2 h = f2_add(make_float2(v[e], v[e + 1]), make_float2(r[e], r[e + 1]));
+      v[e] = h.x;
+      v[e + 1] = h.y;
+    }
   };
   auto store_h = [&](int c, const float (&v)[kMxChunk]) {
     if (p.res_f32)
@@ -437,14 +465,22 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
   };
   auto squares = [&](const float (&v)[kMxChunk]) {
     // four sums of four: short chains keep the rounding small
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float2 s[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-    for (int e = 0; e < kMxChunk; ++e) s[e & 3] = __fmaf_rn(v[e], v[e], s[e & 3]);
-    return (s[0] + s[1]) + (s[2] + s[3]);
+    for (int e = 0; e < kMxChunk; e += 2) {
+      const float2 x = make_float2(v[e], v[e + 1]);
+      s[(e >> 1) & 1] = f2_fma(x, x, s[(e >> 1) & 1]);
+    }
+    return (s[0].x + s[0].y) + (s[1].x + s[1].y);
   };
   auto scaled = [&](int c, float rstd, const float (&w)[kMxChunk], float (&v)[kMxChunk]) {
 #pragma unroll
-    for (int e = 0; e < kMxChunk; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], rstd), w[e]);
+    for (int e = 0; e < kMxChunk; e += 2) {
+      const float2 r =
+          f2_mul(f2_mul(make_float2(v[e], v[e + 1]), make_float2(rstd, rstd)), make_float2(w[e], w[e + 1]));
+      v[e] = r.x;
+      v[e + 1] = r.y;
+    }
     if (kMxChunk * c + kMxChunk > p.K) {         // past K: not 0 * infinity
 #pragma unroll
       for (int e = 0; e < kMxChunk; ++e)
@@ -488,15 +524,16 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
         scaled(t + j * TPR, rstd, f, v[j]);
       }
     }
-    uint32_t amax = 0;
-    if constexpr (FMT == kNvFp4) {
+    uint32_t amax[NCH], top = 0;
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) amax = max(amax, chunk_amax(v[j]));
-      amax = row_max<TPR>(amax, red_max);
+    for (int j = 0; j < NCH; ++j) {
+      amax[j] = chunk_amax(v[j]);
+      top = max(top, amax[j]);
     }
+    if constexpr (FMT == kNvFp4) top = row_max<TPR>(top, red_max);
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) emit_chunk<FMT>(p, codes, words, t + j * TPR, v[j], amax);
-    store_row_scale(amax);
+    for (int j = 0; j < NCH; ++j) emit_chunk<FMT>(p, codes, words, t + j * TPR, v[j], amax[j], top);
+    store_row_scale(top);
   } else {
     static_assert(NCH == 1, "one chunk per pass");
     // a whole number of passes for every thread: the shuffles need full warps
@@ -539,7 +576,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
       load_h(t + i * TPR, v);
       if (res) store_h(t + i * TPR, v[0]);
       if constexpr (kNorm) normed(t + i * TPR, rstd, v[0]);
-      emit_chunk<FMT>(p, codes, words, t + i * TPR, v[0], amax);
+      emit_chunk<FMT>(p, codes, words, t + i * TPR, v[0], chunk_amax(v[0]), amax);
     }
     store_row_scale(amax);
   }

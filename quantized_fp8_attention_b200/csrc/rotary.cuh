@@ -100,8 +100,13 @@ struct RotRaw {
 // lanes with 4 + 4 channels, 8 bytes an access, ran at 3.9 instead of 5.8
 // TB/s).  Rows are fetched one batch ahead: the first while the angles are
 // formed, the next while one is rotated.
-template <typename T, bool kSplit>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) rotary_kernel(const __grid_constant__ RotaryParams p) {
+// kNorm: a weight is given for Q or K.  The weight goes into the coefficients
+// of the rotation, so a row costs its sum of squares, one factor and the
+// rotation; two pairs share each packed instruction.  (Unpacked, with weights
+// applied per row, the kernel was bound by its 193 instructions per row and
+// warp.)  kAll: all 64 pairs rotate.
+template <typename T, bool kSplit, bool kNorm, bool kAll>
+__global__ void __launch_bounds__(256, sizeof(T) == 4 || (kSplit && kNorm) ? 2 : 3) rotary_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int LPR = kSplit ? 8 : 16;                 // lanes per row
   constexpr int P = kSplit ? 8 : 4;                    // channels per piece = pairs per lane
   constexpr int HS = 16 / LPR;                         // heads at a time
@@ -158,14 +163,31 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) rotary_kernel(con
     const int first = max(h0, base), last = min(h1, base + p.heads[part]);
     if (first >= last) continue;
     if (part != part0) fetch(part, first, last, cur);
-    float w[2 * P];
-    const bool norm = p.weight[part] != nullptr;
+    // y0 = x0 a - x1 b, y1 = x0 c + x1 d for pairs 2i, 2i + 1 of the lane
+    float2 ca[P / 2], cb[P / 2], cc[P / 2], cd[P / 2];
+    const bool norm = kNorm && p.weight[part] != nullptr;
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      ca[i] = cd[i] = make_float2(cs[2 * i], cs[2 * i + 1]);
+      cc[i] = make_float2(sn[2 * i], sn[2 * i + 1]);
+      cb[i] = make_float2(-sn[2 * i], -sn[2 * i + 1]);
+    }
     if (norm) {
       const T* wp = static_cast<const T*>(p.weight[part]);
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        w[e] = to_f32<T>(wp[c0 + e]);
-        w[P + e] = to_f32<T>(wp[c1 + e]);
+      for (int i = 0; i < P / 2; ++i) {
+        float2 w0, w1;                 // of the first and second channels of the two pairs
+        if constexpr (kSplit) {
+          w0 = make_float2(to_f32<T>(wp[c0 + 2 * i]), to_f32<T>(wp[c0 + 2 * i + 1]));
+          w1 = make_float2(to_f32<T>(wp[c1 + 2 * i]), to_f32<T>(wp[c1 + 2 * i + 1]));
+        } else {
+          w0 = make_float2(to_f32<T>(wp[c0 + 4 * i]), to_f32<T>(wp[c0 + 4 * i + 2]));
+          w1 = make_float2(to_f32<T>(wp[c0 + 4 * i + 1]), to_f32<T>(wp[c0 + 4 * i + 3]));
+        }
+        ca[i] = f2_mul(ca[i], w0);
+        cc[i] = f2_mul(cc[i], w0);
+        cb[i] = f2_mul(cb[i], w1);
+        cd[i] = f2_mul(cd[i], w1);
       }
     }
     T* out = static_cast<T*>(p.out[part]) + ((int64_t)b * p.heads[part] * p.N + n) * kHeadDim;
@@ -179,23 +201,43 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) rotary_kernel(con
         const int hh = h + u * HS + sub;
         float v[2 * P];
         cur[u].get(v);
-        if (norm) {
-          float ss = 0.0f;
+        // x0 and x1 of pairs 2i, 2i + 1
+        float2 x0[P / 2], x1[P / 2];
 #pragma unroll
-          for (int e = 0; e < 2 * P; ++e) ss += v[e] * v[e];
+        for (int i = 0; i < P / 2; ++i) {
+          x0[i] = kSplit ? make_float2(v[2 * i], v[2 * i + 1]) : make_float2(v[4 * i], v[4 * i + 2]);
+          x1[i] = kSplit ? make_float2(v[P + 2 * i], v[P + 2 * i + 1]) : make_float2(v[4 * i + 1], v[4 * i + 3]);
+        }
+        if (norm) {
+          float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i) s2 = f2_fma(x1[i], x1[i], f2_fma(x0[i], x0[i], s2));
+          float ss = s2.x + s2.y;
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-          const float r = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
+          const float r = rsqrtf(fmaf(ss, 1.0f / kHeadDim, p.eps));
 #pragma unroll
-          for (int e = 0; e < 2 * P; ++e) v[e] = v[e] * r * w[e];
+          for (int i = 0; i < P / 2; ++i) {
+            x0[i] = f2_mul(x0[i], make_float2(r, r));
+            x1[i] = f2_mul(x1[i], make_float2(r, r));
+          }
         }
         float y[2 * P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const int a = kSplit ? i : 2 * i, d = kSplit ? P + i : 2 * i + 1;
-          const bool on = kSplit ? rotates : P * l + i < p.pairs;
-          y[a] = on ? v[a] * cs[i] - v[d] * sn[i] : v[a];
-          y[d] = on ? v[a] * sn[i] + v[d] * cs[i] : v[d];
+        for (int i = 0; i < P / 2; ++i) {
+          float2 y0 = f2_fma(x0[i], ca[i], f2_mul(x1[i], cb[i])), y1 = f2_fma(x0[i], cc[i], f2_mul(x1[i], cd[i]));
+          if constexpr (!kAll) {       // a channel that does not rotate takes nothing from its neighbour
+            const bool on0 = kSplit ? rotates : P * l + 2 * i < p.pairs;
+            const bool on1 = kSplit ? rotates : P * l + 2 * i + 1 < p.pairs;
+            y0.x = on0 ? y0.x : x0[i].x * (norm ? ca[i].x : 1.0f);
+            y1.x = on0 ? y1.x : x1[i].x * (norm ? cd[i].x : 1.0f);
+            y0.y = on1 ? y0.y : x0[i].y * (norm ? ca[i].y : 1.0f);
+            y1.y = on1 ? y1.y : x1[i].y * (norm ? cd[i].y : 1.0f);
+          }
+          y[kSplit ? 2 * i : 4 * i] = y0.x;
+          y[kSplit ? 2 * i + 1 : 4 * i + 2] = y0.y;
+          y[kSplit ? P + 2 * i : 4 * i + 1] = y1.x;
+          y[kSplit ? P + 2 * i + 1 : 4 * i + 3] = y1.y;
         }
         if (here && hh < last) {
           T* dst = out + (int64_t)(hh - base) * p.N * kHeadDim;
