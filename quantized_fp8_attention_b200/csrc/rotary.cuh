@@ -42,75 +42,41 @@ struct RotaryParams {
   uint8_t axis[64];
 };
 
-// A lane's channels of a row, two pieces of P, as they lie in memory.
-template <typename T, int P>
-struct RotRaw {
-  static constexpr int kWords = P * sizeof(T) / 4;      // of a piece
-  uint32_t w[2 * kWords];
-  __device__ __forceinline__ void piece(const T* p, int at) {
-    if constexpr (kWords % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < kWords; i += 4) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p + i * 4 / sizeof(T));
-        w[at + i] = a.x; w[at + i + 1] = a.y; w[at + i + 2] = a.z; w[at + i + 3] = a.w;
-      }
-    } else {
-      static_assert(kWords == 2, "8 or 16 bytes");
-      const uint2 a = *reinterpret_cast<const uint2*>(p);
-      w[at] = a.x; w[at + 1] = a.y;
-    }
-  }
-  // kJoined: the pieces are neighbours
-  template <bool kJoined>
-  __device__ __forceinline__ void load(const T* row, int c0, int c1, bool vec) {
-    if (vec) {
-      if constexpr (kJoined && kWords == 2) {
-        const uint4 a = *reinterpret_cast<const uint4*>(row + c0);
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      } else {
-        piece(row + c0, 0);
-        piece(row + c1, kWords);
-      }
-    } else {
-      T e[2 * P];
-#pragma unroll
-      for (int i = 0; i < 2 * P; ++i) e[i] = row[i < P ? c0 + i : c1 + i - P];
-#pragma unroll
-      for (int i = 0; i < 2 * kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(e)[i];
-    }
-  }
-  __device__ __forceinline__ void get(float (&v)[2 * P]) const {
-#pragma unroll
-    for (int i = 0; i < 2 * kWords; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        v[i] = __uint_as_float(w[i]);
-      } else {
-        const float2 f = unpack2<T>(w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      }
-    }
-  }
-};
+// Asynchronous copy of 16 bytes, global to shared (both on 16-byte boundaries).
+__device__ __forceinline__ void cp_async_16(uint32_t smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // kSplit: pair j is channels (j, pairs + j); otherwise (2j, 2j + 1).  Pairs
 // never cross lanes: interleaved a lane of 16 holds eight neighbours (four
 // pairs); split a lane of 8 holds eight channels and their eight partners, and
 // the 16 lanes take two heads at a time.  Every access is 16 bytes a lane (16
 // lanes with 4 + 4 channels, 8 bytes an access, ran at 3.9 instead of 5.8
-// TB/s).  Rows are fetched one batch ahead: the first while the angles are
-// formed, the next while one is rotated.
+// TB/s).  Rows are fetched ahead by asynchronous copies into a ring of shared
+// memory in which every thread reads only what it copied itself, so there is no
+// barrier: two batches of 64 bytes a thread are in flight whatever the register
+// count (one batch ahead in registers: 4608 tokens x 48 heads took 29 us, half
+// the memory's rate).
 // kNorm: a weight is given for Q or K.  The weight goes into the coefficients
 // of the rotation, so a row costs its sum of squares, one factor and the
 // rotation; two pairs share each packed instruction.  (Unpacked, with weights
 // applied per row, the kernel was bound by its 193 instructions per row and
 // warp.)  kAll: all 64 pairs rotate.
 template <typename T, bool kSplit, bool kNorm, bool kAll>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 || (kSplit && kNorm) ? 2 : 3) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(256, kSplit ? (kNorm ? 2 : 3) : (kNorm ? 3 : 4)) rotary_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int LPR = kSplit ? 8 : 16;                 // lanes per row
   constexpr int P = kSplit ? 8 : 4;                    // channels per piece = pairs per lane
   constexpr int HS = 16 / LPR;                         // heads at a time
-  constexpr int U = (kSplit ? 2 : 4) / (sizeof(T) == 4 ? 2 : 1);   // batch: U * HS heads
+  constexpr int U = (kSplit ? 2 : 4) / (sizeof(T) == 4 ? 2 : 1);   // batch: U * HS heads, 64 bytes a thread
+  constexpr int V = P * sizeof(T) / 8;                 // 16-byte groups of a lane per row
+  constexpr int D = 3;                                 // batches in the ring
+  static_assert(U * V == 4, "64 bytes");
+  __shared__ uint4 ring[D][4][256];
   const int l = threadIdx.x & (LPR - 1), sub = (threadIdx.x & 15) / LPR;
   const int64_t token = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   const bool here = token < (int64_t)p.B * p.N;
@@ -123,25 +89,41 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || (kSplit && kNorm) ? 2 :
 
   const int total = p.heads[0] + p.heads[1];
   const int h0 = blockIdx.y * p.heads_per_group, h1 = min(total, h0 + p.heads_per_group);
-  RotRaw<T, P> cur[U];
-  // rows h + sub, h + HS + sub, .. (below `last`) of Q or K
-  auto fetch = [&](int part, int h, int last, RotRaw<T, P> (&raw)[U]) {
-    const T* in = static_cast<const T*>(p.in[part]) + (int64_t)b * p.sb[part] + (int64_t)n * p.sn[part];
-    const int base = part ? p.heads[0] : 0;
+  // this group's batches: first those of Q, then those of K
+  const int first0 = min(h0, p.heads[0]), last0 = min(h1, p.heads[0]);
+  const int first1 = max(h0, p.heads[0]), last1 = max(h1, p.heads[0]);
+  const int nb0 = (last0 - first0 + U * HS - 1) / (U * HS), nb = nb0 + (last1 - first1 + U * HS - 1) / (U * HS);
+  auto fetch = [&](int t) {
+    if (t < nb && here) {
+      const int part = t < nb0 ? 0 : 1;
+      const int h = part ? first1 + (t - nb0) * U * HS : first0 + t * U * HS, last = part ? last1 : last0;
+      const T* in = static_cast<const T*>(p.in[part]) + (int64_t)b * p.sb[part] + (int64_t)n * p.sn[part];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int hh = h + u * HS + sub;
-      if (here && hh < last)
-        raw[u].template load<!kSplit>(in + (int64_t)(hh - base) * p.sh[part], c0, c1, p.vec[part]);
+      for (int u = 0; u < U; ++u) {
+        const int hh = h + u * HS + sub;
+        if (hh >= last) break;
+        const T* row = in + (int64_t)(hh - (part ? p.heads[0] : 0)) * p.sh[part];
+        uint4* to = &ring[t % D][u * V][threadIdx.x];
+        if (p.vec[part]) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {                // group i: channels of the first piece, then the second
+            constexpr int G = 16 / sizeof(T);
+            const int c = i * G < P ? c0 + i * G : c1 + i * G - P;
+            cp_async_16(smem_u32(to + i * 256), row + c);
+          }
+        } else {
+          alignas(16) T e[2 * P];
+#pragma unroll
+          for (int i = 0; i < 2 * P; ++i) e[i] = row[i < P ? c0 + i : c1 + i - P];
+#pragma unroll
+          for (int i = 0; i < V; ++i) to[i * 256] = reinterpret_cast<const uint4*>(e)[i];
+        }
+      }
     }
+    cp_async_commit();
   };
-  const int part0 = h0 < p.heads[0] ? 0 : 1;
-  const int last0 = part0 ? h1 : min(h1, p.heads[0]);
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int i = 0; i < RotRaw<T, P>::kWords * 2; ++i) cur[u].w[i] = 0u;
-  fetch(part0, h0, last0, cur);
+  fetch(0);
+  fetch(1);
 
   float cs[P], sn[P];
 #pragma unroll
@@ -158,14 +140,11 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || (kSplit && kNorm) ? 2 :
     }
   }
 
-  for (int part = part0; part < 2; ++part) {
-    const int base = part ? p.heads[0] : 0;
-    const int first = max(h0, base), last = min(h1, base + p.heads[part]);
-    if (first >= last) continue;
-    if (part != part0) fetch(part, first, last, cur);
+  float2 ca[P / 2], cb[P / 2], cc[P / 2], cd[P / 2];
+  bool norm = false;
+  auto coefficients = [&](int part) {
     // y0 = x0 a - x1 b, y1 = x0 c + x1 d for pairs 2i, 2i + 1 of the lane
-    float2 ca[P / 2], cb[P / 2], cc[P / 2], cd[P / 2];
-    const bool norm = kNorm && p.weight[part] != nullptr;
+    norm = kNorm && p.weight[part] != nullptr;
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) {
       ca[i] = cd[i] = make_float2(cs[2 * i], cs[2 * i + 1]);
@@ -190,69 +169,83 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || (kSplit && kNorm) ? 2 :
         cd[i] = f2_mul(cd[i], w1);
       }
     }
-    T* out = static_cast<T*>(p.out[part]) + ((int64_t)b * p.heads[part] * p.N + n) * kHeadDim;
-    for (int h = first; h < last; h += U * HS) {
-      RotRaw<T, P> next[U];
+  };
+
+  for (int t = 0; t < nb; ++t) {
+    fetch(t + 2);
+    const int part = t < nb0 ? 0 : 1;
+    if (t == 0 || t == nb0) coefficients(part);
+    const int h = part ? first1 + (t - nb0) * U * HS : first0 + t * U * HS, last = part ? last1 : last0;
+    T* out = static_cast<T*>(p.out[part]) +
+             (((int64_t)b * p.heads[part] + h + sub - (part ? p.heads[0] : 0)) * p.N + n) * kHeadDim;
+    cp_async_wait<2>();                // all but the two batches fetched last
 #pragma unroll
-      for (int u = 0; u < U; ++u) next[u] = cur[u];
-      if (h + U * HS < last) fetch(part, h + U * HS, last, next);
+    for (int u = 0; u < U; ++u) {
+      float v[2 * P];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int hh = h + u * HS + sub;
-        float v[2 * P];
-        cur[u].get(v);
-        // x0 and x1 of pairs 2i, 2i + 1
-        float2 x0[P / 2], x1[P / 2];
+      for (int i = 0; i < V; ++i) {
+        const uint4 g = ring[t % D][u * V + i][threadIdx.x];
+        const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-        for (int i = 0; i < P / 2; ++i) {
-          x0[i] = kSplit ? make_float2(v[2 * i], v[2 * i + 1]) : make_float2(v[4 * i], v[4 * i + 2]);
-          x1[i] = kSplit ? make_float2(v[P + 2 * i], v[P + 2 * i + 1]) : make_float2(v[4 * i + 1], v[4 * i + 3]);
-        }
-        if (norm) {
-          float2 s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int i = 0; i < P / 2; ++i) s2 = f2_fma(x1[i], x1[i], f2_fma(x0[i], x0[i], s2));
-          float ss = s2.x + s2.y;
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-          const float r = rsqrtf(fmaf(ss, 1.0f / kHeadDim, p.eps));
-#pragma unroll
-          for (int i = 0; i < P / 2; ++i) {
-            x0[i] = f2_mul(x0[i], make_float2(r, r));
-            x1[i] = f2_mul(x1[i], make_float2(r, r));
-          }
-        }
-        float y[2 * P];
-#pragma unroll
-        for (int i = 0; i < P / 2; ++i) {
-          float2 y0 = f2_fma(x0[i], ca[i], f2_mul(x1[i], cb[i])), y1 = f2_fma(x0[i], cc[i], f2_mul(x1[i], cd[i]));
-          if constexpr (!kAll) {       // a channel that does not rotate takes nothing from its neighbour
-            const bool on0 = kSplit ? rotates : P * l + 2 * i < p.pairs;
-            const bool on1 = kSplit ? rotates : P * l + 2 * i + 1 < p.pairs;
-            y0.x = on0 ? y0.x : x0[i].x * (norm ? ca[i].x : 1.0f);
-            y1.x = on0 ? y1.x : x1[i].x * (norm ? cd[i].x : 1.0f);
-            y0.y = on1 ? y0.y : x0[i].y * (norm ? ca[i].y : 1.0f);
-            y1.y = on1 ? y1.y : x1[i].y * (norm ? cd[i].y : 1.0f);
-          }
-          y[kSplit ? 2 * i : 4 * i] = y0.x;
-          y[kSplit ? 2 * i + 1 : 4 * i + 2] = y0.y;
-          y[kSplit ? P + 2 * i : 4 * i + 1] = y1.x;
-          y[kSplit ? P + 2 * i + 1 : 4 * i + 3] = y1.y;
-        }
-        if (here && hh < last) {
-          T* dst = out + (int64_t)(hh - base) * p.N * kHeadDim;
-          uint32_t q[RotRaw<T, P>::kWords * 2];
-          pack_words<T, 2 * P>(y, q);
-          constexpr int W = RotRaw<T, P>::kWords;
-#pragma unroll
-          for (int i = 0; i < 2 * W; i += 4) {         // (a 16-byte store may span two neighbouring pieces)
-            T* at = dst + (i < W ? c0 : c1 - P) + i * 4 / (int)sizeof(T);
-            *reinterpret_cast<uint4*>(at) = make_uint4(q[i], q[i + 1], q[i + 2], q[i + 3]);
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (sizeof(T) == 4) {
+            v[4 * i + e] = __uint_as_float(w[e]);
+          } else {
+            const float2 f = unpack2<T>(w[e]);
+            v[8 * i + 2 * e] = f.x;
+            v[8 * i + 2 * e + 1] = f.y;
           }
         }
       }
+      // x0 and x1 of pairs 2i, 2i + 1
+      float2 x0[P / 2], x1[P / 2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) cur[u] = next[u];
+      for (int i = 0; i < P / 2; ++i) {
+        x0[i] = kSplit ? make_float2(v[2 * i], v[2 * i + 1]) : make_float2(v[4 * i], v[4 * i + 2]);
+        x1[i] = kSplit ? make_float2(v[P + 2 * i], v[P + 2 * i + 1]) : make_float2(v[4 * i + 1], v[4 * i + 3]);
+      }
+      if (norm) {
+        float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) s2 = f2_fma(x1[i], x1[i], f2_fma(x0[i], x0[i], s2));
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        const float r = rsqrtf(fmaf(ss, 1.0f / kHeadDim, p.eps));
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) {
+          x0[i] = f2_mul(x0[i], make_float2(r, r));
+          x1[i] = f2_mul(x1[i], make_float2(r, r));
+        }
+      }
+      float y[2 * P];
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) {
+        float2 y0 = f2_fma(x0[i], ca[i], f2_mul(x1[i], cb[i])), y1 = f2_fma(x0[i], cc[i], f2_mul(x1[i], cd[i]));
+        if constexpr (!kAll) {       // a channel that does not rotate takes nothing from its neighbour
+          const bool on0 = kSplit ? rotates : P * l + 2 * i < p.pairs;
+          const bool on1 = kSplit ? rotates : P * l + 2 * i + 1 < p.pairs;
+          y0.x = on0 ? y0.x : x0[i].x * (norm ? ca[i].x : 1.0f);
+          y1.x = on0 ? y1.x : x1[i].x * (norm ? cd[i].x : 1.0f);
+          y0.y = on1 ? y0.y : x0[i].y * (norm ? ca[i].y : 1.0f);
+          y1.y = on1 ? y1.y : x1[i].y * (norm ? cd[i].y : 1.0f);
+        }
+        y[kSplit ? 2 * i : 4 * i] = y0.x;
+        y[kSplit ? 2 * i + 1 : 4 * i + 2] = y0.y;
+        y[kSplit ? P + 2 * i : 4 * i + 1] = y1.x;
+        y[kSplit ? P + 2 * i + 1 : 4 * i + 3] = y1.y;
+      }
+      if (here && h + u * HS + sub < last) {
+        T* dst = out + (int64_t)u * HS * p.N * kHeadDim;
+        uint32_t q[4 * V];
+        pack_words<T, 2 * P>(y, q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          constexpr int G = 16 / sizeof(T);
+          T* at = dst + (i * G < P ? c0 + i * G : c1 + i * G - P);
+          *reinterpret_cast<uint4*>(at) = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+        }
+      }
     }
   }
 }
