@@ -249,57 +249,61 @@ static size_t dtype_bytes(int t) { return t == FQA_DTYPE_F32 ? 4 : 2; }
 // One launch of the row kernel that fits the row: 16 elements a thread and
 // chunk, two chunks in registers (one of binary32: 103 registers a thread left
 // two CTAs per SM, 23 us for 1023 x 5100).  Threads per row by its length: a
-// warp for short ones (no block-wide sums), then 128, 256 and 512; longer rows,
-// and rows off the 16-byte boundaries, are read again for each step.
+// warp for short ones (no block-wide sums), then 128, 256 and 512; longer rows
+// are read again for each step.  Rows off the 16-byte boundaries go through
+// shared memory while they fit there.
 template <typename T, int FMT, bool kNorm>
-static void launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s) {
+static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s) {
   constexpr int NCH = sizeof(T) == 4 ? 1 : 2;
-  const int threads = p.KT * MxTraits<FMT>::kWordChunks / NCH;   // that hold the row's words, whole
-  if (!vec)
-    mx_row_kernel<T, FMT, kNorm, 128, 1, true, false><<<p.M, 128, 0, s>>>(p);
-  else if (threads <= 32)
+  const int chunks = p.KT * MxTraits<FMT>::kWordChunks;
+  const int threads = chunks / NCH;              // that hold the row's words, whole
+  if (!vec && chunks * kMxChunk <= kMxAnyCols) {
+    const int smem = chunks * kMxChunk * 4;
+    const auto fn = mx_row_any_kernel<T, FMT, kNorm>;
+    if (smem > 48 * 1024 && cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kMxAnyCols * 4) != cudaSuccess)
+      return FQA_ERR_CUDA;
+    fn<<<p.M, kMxAnyThreads, smem, s>>>(p);
+  } else if (!vec) {
+    mx_row_kernel<T, FMT, kNorm, 512, 1, true, false><<<p.M, 512, 0, s>>>(p);
+  } else if (threads <= 32) {
     mx_row_kernel<T, FMT, kNorm, 32, NCH, false, true><<<(p.M + 3) / 4, 128, 0, s>>>(p);
-  else if (threads <= 128)
+  } else if (threads <= 128) {
     mx_row_kernel<T, FMT, kNorm, 128, NCH, false, true><<<p.M, 128, 0, s>>>(p);
-  else if (threads <= 256)
+  } else if (threads <= 256) {
     mx_row_kernel<T, FMT, kNorm, 256, NCH, false, true><<<p.M, 256, 0, s>>>(p);
-  else if (threads <= 512)
+  } else if (threads <= 512) {
     mx_row_kernel<T, FMT, kNorm, 512, NCH, false, true><<<p.M, 512, 0, s>>>(p);
-  else
+  } else {
     mx_row_kernel<T, FMT, kNorm, 512, 1, true, true><<<p.M, 512, 0, s>>>(p);
+  }
+  return launch_status();
 }
 
 template <typename T, bool kNorm>
-static void launch_mx_format(const MxRowParams& p, int fmt, bool vec, cudaStream_t s) {
-  if (fmt == FQA_MXFP8)
-    launch_mx_rows<T, kMxFp8, kNorm>(p, vec, s);
-  else if (fmt == FQA_MXFP4)
-    launch_mx_rows<T, kMxFp4, kNorm>(p, vec, s);
-  else
-    launch_mx_rows<T, kNvFp4, kNorm>(p, vec, s);
+static fqa_status launch_mx_format(const MxRowParams& p, int fmt, bool vec, cudaStream_t s) {
+  if (fmt == FQA_MXFP8) return launch_mx_rows<T, kMxFp8, kNorm>(p, vec, s);
+  if (fmt == FQA_MXFP4) return launch_mx_rows<T, kMxFp4, kNorm>(p, vec, s);
+  return launch_mx_rows<T, kNvFp4, kNorm>(p, vec, s);
 }
 
 template <bool kNorm>
 static fqa_status launch_mx(const MxRowParams& p, int dtype, int fmt, bool vec, cudaStream_t s) {
-  if (dtype == FQA_DTYPE_BF16)
-    launch_mx_format<__nv_bfloat16, kNorm>(p, fmt, vec, s);
-  else if (dtype == FQA_DTYPE_F16)
-    launch_mx_format<__half, kNorm>(p, fmt, vec, s);
-  else
-    launch_mx_format<float, kNorm>(p, fmt, vec, s);
-  return launch_status();
+  if (dtype == FQA_DTYPE_BF16) return launch_mx_format<__nv_bfloat16, kNorm>(p, fmt, vec, s);
+  if (dtype == FQA_DTYPE_F16) return launch_mx_format<__half, kNorm>(p, fmt, vec, s);
+  return launch_mx_format<float, kNorm>(p, fmt, vec, s);
 }
 
 template <typename T, int FMT>
 static void launch_mx_dequantize(const MxDequantParams& p, bool vec, cudaStream_t s) {
-  const int chunks = (p.K + kMxChunk - 1) / kMxChunk;
-  int tx = 4;                            // chunks side by side: a power of two, up to a whole CTA
-  while (tx < chunks && tx < 256) tx *= 2;
+  const int items = (p.K + (vec ? kMxChunk : 2) - 1) / (vec ? kMxChunk : 2);
+  int tx = 4;                            // items side by side: a power of two, up to a whole CTA
+  while (tx < items && tx < 256) tx *= 2;
   const dim3 block(tx, 256 / tx), grid((p.M + block.y - 1) / block.y);
   if (vec)
-    mx_dequantize_kernel<T, FMT, true><<<grid, block, 0, s>>>(p);
+    mx_dequantize_kernel<T, FMT><<<grid, block, 0, s>>>(p);
   else
-    mx_dequantize_kernel<T, FMT, false><<<grid, block, 0, s>>>(p);
+    mx_dequantize_any_kernel<T, FMT><<<grid, block, 0, s>>>(p);
 }
 
 template <typename T>

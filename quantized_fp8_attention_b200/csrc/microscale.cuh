@@ -582,6 +582,110 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
   }
 }
 
+// The same for rows off the 16-byte boundaries (an odd K, a shifted view): one
+// row per CTA, read element by element along the row, so that a warp's loads and
+// stores are one segment, into shared memory as binary32; the chunks are taken
+// from there.  (Chunks of 16 straight from memory, element by element, touch a
+// sector per lane and load, and needed the row again for every step.)
+constexpr int kMxAnyThreads = 256;
+constexpr int kMxAnyCols = 49152;            // longest row held
+
+template <typename T, int FMT, bool kNorm>
+__global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowParams p) {
+  extern __shared__ __align__(16) float h[];   // Kw values, zeros past K
+  __shared__ float red_sum[kMxAnyThreads / 32];
+  __shared__ uint32_t red_max[kMxAnyThreads / 32];
+  const int t = threadIdx.x, row = blockIdx.x;
+  const T* x = static_cast<const T*>(p.x) + (int64_t)row * p.ldx;
+  const int chunks = p.KT * MxTraits<FMT>::kWordChunks, width = chunks * kMxChunk;
+  const bool res = kNorm && p.residual != nullptr;
+  float ss = 0.0f;
+  constexpr int B = 8;                           // elements a thread has in flight
+  for (int e0 = t; e0 < p.K; e0 += B * kMxAnyThreads) {
+    T a[B];
+    float r[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int e = e0 + i * kMxAnyThreads;
+      a[i] = e < p.K ? x[e] : from_f32<T>(0.0f);
+    }
+    if (res && p.res_f32) {
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int e = e0 + i * kMxAnyThreads;
+        r[i] = e < p.K ? static_cast<const float*>(p.residual)[(int64_t)row * p.ldr + e] : 0.0f;
+      }
+    } else if (res) {
+      T q[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int e = e0 + i * kMxAnyThreads;
+        q[i] = e < p.K ? static_cast<const T*>(p.residual)[(int64_t)row * p.ldr + e] : from_f32<T>(0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) r[i] = to_f32<T>(q[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int e = e0 + i * kMxAnyThreads;
+      if (e >= p.K) break;
+      float v = to_f32<T>(a[i]);
+      if (res) {
+        v += r[i];
+        if (p.res_f32)
+          static_cast<float*>(p.residual_out)[(int64_t)row * p.K + e] = v;
+        else
+          static_cast<T*>(p.residual_out)[(int64_t)row * p.K + e] = from_f32<T>(v);
+      }
+      h[e] = v;
+      if constexpr (kNorm) ss = fmaf(v, v, ss);
+    }
+  }
+  for (int e = p.K + t; e < width; e += kMxAnyThreads) h[e] = 0.0f;
+  uint32_t top = 0;
+  if constexpr (kNorm) {
+    const float rstd = __frsqrt_rn(__fdiv_rn(row_sum<kMxAnyThreads>(ss, red_sum), (float)p.K) + p.eps);
+    for (int e0 = t; e0 < p.K; e0 += B * kMxAnyThreads) {
+      float w[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int e = e0 + i * kMxAnyThreads;
+        w[i] = 0.0f;
+        if (e < p.K)
+          w[i] = p.w_f32 ? static_cast<const float*>(p.weight)[e] : to_f32<T>(static_cast<const T*>(p.weight)[e]);
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int e = e0 + i * kMxAnyThreads;
+        if (e >= p.K) break;
+        const float y = __fmul_rn(__fmul_rn(h[e], rstd), w[i]);
+        h[e] = y;
+        if constexpr (FMT == kNvFp4) top = max(top, __float_as_uint(y) & 0x7FFFFFFFu);
+      }
+    }
+  } else if constexpr (FMT == kNvFp4) {
+    for (int e = t; e < p.K; e += kMxAnyThreads) top = max(top, __float_as_uint(h[e]) & 0x7FFFFFFFu);
+  }
+  if constexpr (FMT == kNvFp4) top = row_max<kMxAnyThreads>(top, red_max);
+  __syncthreads();
+  uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
+  uint32_t* words = p.scales + (size_t)(row >> 7) * p.KT * 128 + (row & 31) * 4 + ((row >> 5) & 3);
+  for (int c0 = 0; c0 < chunks; c0 += kMxAnyThreads) {      // whole warps: the scales are shared by shuffles
+    const int c = c0 + t;
+    float v[kMxChunk];
+#pragma unroll
+    for (int i = 0; i < kMxChunk; i += 4) {
+      const float4 f = c < chunks ? *reinterpret_cast<const float4*>(h + kMxChunk * c + i)
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
+    }
+    emit_chunk<FMT>(p, codes, words, c, v, chunk_amax(v), top);
+  }
+  if (FMT == kNvFp4 && t == 0)
+    p.row_scale[row] = __uint_as_float(
+        top < 0x7F800000u ? (uint32_t)power_byte(top, 11, 0x280000u, 1) << 23 : 0x7FC00000u);
+}
+
 // ------------------------------------------------------------ and back
 
 // Two E2M1 codes (bits [0,4) and [4,8)) -> their values.
@@ -608,7 +712,7 @@ struct MxDequantParams {
 // value = element * scale (exact in binary32) * row scale, rounded once more to
 // the output's type.  A thread takes chunks of 16 elements, blockDim.x of them
 // side by side in a row and blockDim.y rows per CTA (no division per chunk).
-template <typename T, int FMT, bool kVec>
+template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParams p) {
   constexpr int kBlock = MxTraits<FMT>::kBlock;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
@@ -642,7 +746,30 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParam
     const float s = FMT == kNvFp4 ? e4m3x2_to_f2(sb).x : e8m0_to_f32(sb);
 #pragma unroll
     for (int e = 0; e < kMxChunk; ++e) v[e] = FMT == kNvFp4 ? v[e] * s * rs : v[e] * s;
-    store_chunk<T, kVec>(out, kMxChunk * c, p.K, p.wide, v);
+    store_chunk<T, true>(out, kMxChunk * c, p.K, p.wide, v);
+  }
+}
+
+// The same for rows off the 16-byte boundaries: a thread takes two neighbours,
+// so that a warp's stores are one segment.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantParams p) {
+  constexpr int kBlock = MxTraits<FMT>::kBlock;
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= p.M) return;
+  const uint8_t* sf = p.scales + (size_t)(row >> 7) * p.KT * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+  const uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
+  const float rs = FMT == kNvFp4 ? __ldg(p.row_scale + row) : 1.0f;
+  T* out = static_cast<T*>(p.out) + (int64_t)row * p.K;
+#pragma unroll 4
+  for (int c = threadIdx.x; 2 * c < p.K; c += blockDim.x) {
+    const int blk = 2 * c / kBlock;
+    const uint32_t sb = sf[(size_t)(blk >> 2) * 512 + (blk & 3)];
+    const float2 f = FMT == kMxFp8 ? e4m3x2_to_f2(*reinterpret_cast<const uint16_t*>(codes + 2 * (size_t)c))
+                                   : e2m1x2_to_f2(codes[c]);
+    const float s = FMT == kNvFp4 ? e4m3x2_to_f2(sb).x : e8m0_to_f32(sb);
+    out[2 * c] = from_f32<T>(FMT == kNvFp4 ? f.x * s * rs : f.x * s);
+    if (2 * c + 1 < p.K) out[2 * c + 1] = from_f32<T>(FMT == kNvFp4 ? f.y * s * rs : f.y * s);
   }
 }
 
