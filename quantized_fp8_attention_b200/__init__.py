@@ -27,6 +27,7 @@ FQA_OUT_F16 = 2            # mx_matmul and mx_dequantize only
 HEAD_DIM = 128
 
 _lib = None
+_native = None             # csrc/binding.cpp: the everyday calls without the interpreter
 
 
 def _load():
@@ -94,8 +95,21 @@ def _load():
     L.fqa_rotary.restype = I
     L.fqa_rotary.argtypes = [P, P, I, I, I, I, I, I, Q, Q, Q, Q, Q, Q, P, I, Q, I, P, ctypes.c_double, I, P, P,
                              ctypes.c_float, P, P, P]
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise ImportError(f"_binding.so is not built or does not load ({e}); run "
+                          "`python -m quantized_fp8_attention_b200.build`.") from None
+    _binding.init(LIB_PATH, Microscaled, Rotary)
+    global _native
+    _native = _binding
     _lib = L
     return L
+
+
+def _short_way():
+    _load()
+    return _native
 
 
 class FqaError(RuntimeError):
@@ -717,6 +731,8 @@ def mx_quantize(x: torch.Tensor, fmt: str, out: Optional[Microscaled] = None, st
     """Rows [..., K] of bfloat16, float16 or float32 -> Microscaled rows (leading
     dimensions flattened).  A block (nvfp4: a row) with a NaN or an infinity
     stands for NaN."""
+    if out is None and stream is None and (q := (_native or _short_way()).quantize(x, fmt)) is not None:
+        return q
     index = _device_tensor(x, "x")
     if (there := _elsewhere(index, stream, (x,))) is not None:
         with there:
@@ -735,6 +751,8 @@ def mx_quantize(x: torch.Tensor, fmt: str, out: Optional[Microscaled] = None, st
 def mx_dequantize(q: Microscaled, out_dtype: int = FQA_OUT_BF16, out: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """The values that microscaled rows stand for, [M, cols]."""
+    if out is None and stream is None and (v := (_native or _short_way()).dequantize(q, out_dtype)) is not None:
+        return v
     M, code, index = _require_microscaled(q, "q")
     if (there := _elsewhere(index, stream, q[:3])) is not None:
         with there:
@@ -760,6 +778,9 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, fmt: str = "mxfp8", resid
     [..., K]: (y as Microscaled rows, h in residual's type, or None without a
     residual).  weight [K] and residual are of x's type or float32.
     residual_out may be residual itself (or x, where of the same type)."""
+    if out is None and residual_out is None and stream is None and (
+            y := (_native or _short_way()).rms_norm(x, weight, fmt, residual, eps)) is not None:
+        return y
     index = _device_tensor(x, "x")
     if (there := _elsewhere(index, stream, (x, weight, residual))) is not None:
         with there:
@@ -803,6 +824,8 @@ def mx_matmul(a: Microscaled, b: Microscaled, bias: Optional[torch.Tensor] = Non
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """a [M, K] times the transpose of b [N, K] (a projection's weights), both
     microscaled rows of one format, plus a float32 bias [N]: [M, N]."""
+    if out is None and stream is None and (y := (_native or _short_way()).matmul(a, b, bias, out_dtype)) is not None:
+        return y
     M, code, index = _require_microscaled(a, "a")
     N, other, _ = _require_microscaled(b, "b", index)
     if (there := _elsewhere(index, stream, (*a[:3], *b[:3], bias))) is not None:
@@ -861,6 +884,9 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary, inverse: boo
     adjacent channels; k may be None) -> both normalized (where rot has
     weights) and rotated, contiguous.  `inverse` rotates back.  An output may be
     its own input where that is contiguous."""
+    if q_out is None and k_out is None and stream is None and (
+            y := (_native or _short_way()).rotate(q, k, rot, inverse)) is not None:
+        return y
     index = _device_tensor(q, "q")
     if not isinstance(rot, Rotary):
         raise TypeError(f"rot: expected a Rotary, got {type(rot).__name__}")

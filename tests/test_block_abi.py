@@ -153,3 +153,19 @@ def test_axes():
     for axes, split in (((), False), ((1,), False), ((64, 66), False), ((2,) * 5, False), ((2, 4), True), ((8.0,), False)):
         with pytest.raises(ValueError):
             fqa._axes_array(axes, split)
+
+
+def test_the_short_way_leaves_what_it_does_not_take_to_the_checks(L):
+    """csrc/binding.cpp answers None to anything but the everyday call (here: host
+    tensors, wrong types, wrong counts), and raises nothing."""
+    from quantized_fp8_attention_b200 import _binding as b
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    q = fqa.Microscaled(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 1, 32, 4, 4, dtype=torch.uint8), None, 64,
+                        "mxfp8")
+    rot = fqa.Rotary(torch.zeros(1, 1), (128,))
+    assert b.quantize(x, "mxfp8") is None and b.quantize(x) is None and b.quantize(3, "mxfp8") is None
+    assert b.quantize(x, 7) is None and b.quantize(None, None) is None
+    assert b.dequantize(q, 0) is None and b.dequantize((1, 2), 0) is None and b.dequantize(q, "0") is None
+    assert b.rms_norm(x, x[0], "mxfp8", None, 1e-6) is None and b.rms_norm(x, x[0], "mxfp8", None, 1) is None
+    assert b.matmul(q, q, None, 0) is None and b.matmul(q, None, None, 1 << 70) is None
+    assert b.rotate(x, None, rot, False) is None and b.rotate(x, None, (1, 2), False) is None

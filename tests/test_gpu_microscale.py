@@ -308,3 +308,37 @@ def test_refusals():
                 lambda: f.mx_matmul(q, q, out=h[:, :4]), lambda: f.mx_matmul(q, q, bias=torch.zeros(5, device="cuda"))):
         with pytest.raises((ValueError, TypeError)):
             bad()
+
+
+def test_the_short_way_and_the_checked_one_agree():
+    """The native everyday calls are the ones that run, and give what the Python
+    functions give where an output or a stream sends them the other way."""
+    f = fqa()
+    f.lib()
+    b = f._native
+    x, r = rand(33, 200, "bf16", 1, 1.0), rand(33, 200, "f32", 2, 1.0)
+    w = (1 + 0.1 * torch.randn(200, device="cuda")).bfloat16()
+    bias = torch.randn(33, device="cuda")
+    same = lambda p, q: all((s is None and t is None) or (torch.equal(s, t) if isinstance(s, torch.Tensor) else s == t)
+                            for s, t in zip(p._replace(scales=None), q._replace(scales=None))) and all(
+        np.array_equal(s, t) for s, t in zip(R.held(p)[:2], R.held(q)[:2]))
+    here = torch.cuda.current_stream()
+    for fmt in R.FORMATS:
+        q = b.quantize(x, fmt)
+        assert same(q, f.mx_quantize(x, fmt, stream=here))
+        y, h = b.rms_norm(x, w, fmt, r, 1e-5)
+        y2, h2 = f.mx_rms_norm(x, w, fmt, residual=r, eps=1e-5, stream=here)
+        assert same(y, y2) and torch.equal(h, h2)
+        for t in (0, 1, 2):
+            assert torch.equal(b.dequantize(q, t), f.mx_dequantize(q, t, stream=here))
+            assert torch.equal(b.matmul(y, q, bias, t), f.mx_matmul(y, q, bias=bias, out_dtype=t, stream=here))
+    packed = torch.randn(2, 30, 5, 128, device="cuda").half()
+    q, k = packed[:, :, :3].transpose(1, 2), packed[:, :, 3:].transpose(1, 2)
+    rot = f.Rotary(torch.randint(0, 99, (30, 2), dtype=torch.int32, device="cuda"), (64, 64), split=True,
+                   q_weight=torch.ones(128, device="cuda").half())
+    for got, want in zip(b.rotate(q, k, rot, True), f.rotary(q, k, rot, inverse=True, stream=here)):
+        assert torch.equal(got, want)
+    # not the everyday call
+    assert b.quantize(x[0], "mxfp8") is None and b.quantize(x.T, "mxfp8") is None and b.quantize(x, "mxfp6") is None
+    assert b.matmul(q, q, None, 0) is None and b.matmul(y, y, bias[:3], 0) is None
+    assert b.rotate(q, k[:, :, :3], rot, False) is None and b.rotate(q, k, rot._replace(axes=[64, 64]), False) is None
