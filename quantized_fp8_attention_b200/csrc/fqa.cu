@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -246,6 +247,29 @@ static size_t dtype_bytes(int t) { return t == FQA_DTYPE_F32 ? 4 : 2; }
 
 // -------------------------------------------- launches of microscaled rows
 
+// Launches a kernel that waits for its predecessor itself (grid_wait()), so that
+// its CTAs are scheduled and set up while that one ends; in clusters of
+// `cluster` CTAs.
+template <typename... P, typename... A>
+static fqa_status launch_overlapped(void (*fn)(P...), dim3 grid, dim3 block, int smem, cudaStream_t s, int cluster,
+                                    A&&... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...) != cudaSuccess) return FQA_ERR_CUDA;
+  return launch_status();
+}
+
 // One launch of the row kernel that fits the row: 16 elements a thread and
 // chunk, two chunks in registers (one of binary32: 103 registers a thread left
 // two CTAs per SM, 23 us for 1023 x 5100).  Threads per row by its length: a
@@ -263,21 +287,18 @@ static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s)
     if (smem > 48 * 1024 && cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  kMxAnyCols * 4) != cudaSuccess)
       return FQA_ERR_CUDA;
-    fn<<<p.M, kMxAnyThreads, smem, s>>>(p);
-  } else if (!vec) {
-    mx_row_kernel<T, FMT, kNorm, 512, 1, true, false><<<p.M, 512, 0, s>>>(p);
-  } else if (threads <= 32) {
-    mx_row_kernel<T, FMT, kNorm, 32, NCH, false, true><<<(p.M + 3) / 4, 128, 0, s>>>(p);
-  } else if (threads <= 128) {
-    mx_row_kernel<T, FMT, kNorm, 128, NCH, false, true><<<p.M, 128, 0, s>>>(p);
-  } else if (threads <= 256) {
-    mx_row_kernel<T, FMT, kNorm, 256, NCH, false, true><<<p.M, 256, 0, s>>>(p);
-  } else if (threads <= 512) {
-    mx_row_kernel<T, FMT, kNorm, 512, NCH, false, true><<<p.M, 512, 0, s>>>(p);
-  } else {
-    mx_row_kernel<T, FMT, kNorm, 512, 1, true, true><<<p.M, 512, 0, s>>>(p);
+    return launch_overlapped(fn, p.M, kMxAnyThreads, smem, s, 1, p);
   }
-  return launch_status();
+  if (!vec) return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 512, 1, true, false>, p.M, 512, 0, s, 1, p);
+  if (threads <= 32)
+    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 32, NCH, false, true>, (p.M + 3) / 4, 128, 0, s, 1, p);
+  if (threads <= 128)
+    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 128, NCH, false, true>, p.M, 128, 0, s, 1, p);
+  if (threads <= 256)
+    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 256, NCH, false, true>, p.M, 256, 0, s, 1, p);
+  if (threads <= 512)
+    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 512, NCH, false, true>, p.M, 512, 0, s, 1, p);
+  return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 512, 1, true, true>, p.M, 512, 0, s, 1, p);
 }
 
 template <typename T, bool kNorm>
@@ -295,25 +316,19 @@ static fqa_status launch_mx(const MxRowParams& p, int dtype, int fmt, bool vec, 
 }
 
 template <typename T, int FMT>
-static void launch_mx_dequantize(const MxDequantParams& p, bool vec, cudaStream_t s) {
+static fqa_status launch_mx_dequantize(const MxDequantParams& p, bool vec, cudaStream_t s) {
   const int items = (p.K + (vec ? kMxChunk : 2) - 1) / (vec ? kMxChunk : 2);
   int tx = 4;                            // items side by side: a power of two, up to a whole CTA
   while (tx < items && tx < 256) tx *= 2;
   const dim3 block(tx, 256 / tx), grid((p.M + block.y - 1) / block.y);
-  if (vec)
-    mx_dequantize_kernel<T, FMT><<<grid, block, 0, s>>>(p);
-  else
-    mx_dequantize_any_kernel<T, FMT><<<grid, block, 0, s>>>(p);
+  return launch_overlapped(vec ? mx_dequantize_kernel<T, FMT> : mx_dequantize_any_kernel<T, FMT>, grid, block, 0, s, 1, p);
 }
 
 template <typename T>
-static void launch_mx_dequantize_format(const MxDequantParams& p, int fmt, bool vec, cudaStream_t s) {
-  if (fmt == FQA_MXFP8)
-    launch_mx_dequantize<T, kMxFp8>(p, vec, s);
-  else if (fmt == FQA_MXFP4)
-    launch_mx_dequantize<T, kMxFp4>(p, vec, s);
-  else
-    launch_mx_dequantize<T, kNvFp4>(p, vec, s);
+static fqa_status launch_mx_dequantize_format(const MxDequantParams& p, int fmt, bool vec, cudaStream_t s) {
+  if (fmt == FQA_MXFP8) return launch_mx_dequantize<T, kMxFp8>(p, vec, s);
+  if (fmt == FQA_MXFP4) return launch_mx_dequantize<T, kMxFp4>(p, vec, s);
+  return launch_mx_dequantize<T, kNvFp4>(p, vec, s);
 }
 
 template <int FMT, int NT>
@@ -335,19 +350,8 @@ static fqa_status launch_mx_small(const uint8_t* a, const uint8_t* b, const MxMa
   const auto fn = mx_matmul_small_kernel<FMT, NT>;
   if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess)
     return FQA_ERR_CUDA;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ranks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * ranks));
-  cfg.blockDim = dim3(kMxSmallThreads);
-  cfg.dynamicSmemBytes = T::kSmemBytes;
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, tp, tq, p, ranks) != cudaSuccess) return FQA_ERR_CUDA;
-  return launch_status();
+  return launch_overlapped(fn, dim3((unsigned)(tiles * ranks)), kMxSmallThreads, T::kSmemBytes, s, ranks, tp, tq, p,
+                           ranks);
 }
 
 template <int FMT>
@@ -367,19 +371,8 @@ static fqa_status launch_mx_large(const uint8_t* a, const uint8_t* b, const MxMa
   const auto fn = mx_matmul_large_kernel<FMT>;
   if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess)
     return FQA_ERR_CUDA;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(tiles, num_sms() / 2));
-  cfg.blockDim = dim3(kMxLargeThreads);
-  cfg.dynamicSmemBytes = T::kSmemBytes;
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, ta, tb, tsa, tsb, to, p, (int)tma_out) != cudaSuccess) return FQA_ERR_CUDA;
-  return launch_status();
+  return launch_overlapped(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, num_sms() / 2)), kMxLargeThreads,
+                           T::kSmemBytes, s, 2, ta, tb, tsa, tsb, to, p, (int)tma_out);
 }
 
 // The kernel by the product's size: the narrowest tile of tokens that holds
@@ -398,14 +391,14 @@ static fqa_status launch_mx_matmul(const uint8_t* a, const uint8_t* b, const MxM
 }
 
 template <typename T>
-static void launch_rotary(const RotaryParams& p, bool split, bool norm, dim3 grid, cudaStream_t s) {
+static fqa_status launch_rotary(const RotaryParams& p, bool split, bool norm, dim3 grid, cudaStream_t s) {
   using Fn = void (*)(const RotaryParams);
   const bool all = p.pairs == kHeadDim / 2;
   const Fn fns[2][2][2] = {{{rotary_kernel<T, false, false, false>, rotary_kernel<T, false, false, true>},
                             {rotary_kernel<T, false, true, false>, rotary_kernel<T, false, true, true>}},
                            {{rotary_kernel<T, true, false, false>, rotary_kernel<T, true, false, true>},
                             {rotary_kernel<T, true, true, false>, rotary_kernel<T, true, true, true>}}};
-  fns[split][norm][all]<<<grid, 256, 0, s>>>(p);
+  return launch_overlapped(fns[split][norm][all], grid, 256, 0, s, 1, p);
 }
 
 }  // namespace fqa
@@ -897,13 +890,9 @@ fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const 
   const int vec = rows_vectorize(out, K, K, dtype_bytes(out_dtype));
   const MxDequantParams p{codes, scales, row_scale, out, M, K, mx_padded(K), mx_words(K, fmt), vec == 32};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  if (out_dtype == FQA_DTYPE_BF16)
-    launch_mx_dequantize_format<__nv_bfloat16>(p, fmt, vec != 0, s);
-  else if (out_dtype == FQA_DTYPE_F16)
-    launch_mx_dequantize_format<__half>(p, fmt, vec != 0, s);
-  else
-    launch_mx_dequantize_format<float>(p, fmt, vec != 0, s);
-  return launch_status();
+  if (out_dtype == FQA_DTYPE_BF16) return launch_mx_dequantize_format<__nv_bfloat16>(p, fmt, vec != 0, s);
+  if (out_dtype == FQA_DTYPE_F16) return launch_mx_dequantize_format<__half>(p, fmt, vec != 0, s);
+  return launch_mx_dequantize_format<float>(p, fmt, vec != 0, s);
 }
 
 fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,
@@ -1014,13 +1003,9 @@ fqa_status fqa_rotary(const void* q, const void* k, fqa_dtype dtype, int B, int 
   const dim3 grid((unsigned)blocks, (unsigned)((total + p.heads_per_group - 1) / p.heads_per_group));
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool norm = q_weight != nullptr || k_weight != nullptr;
-  if (dtype == FQA_DTYPE_BF16)
-    launch_rotary<__nv_bfloat16>(p, split, norm, grid, s);
-  else if (dtype == FQA_DTYPE_F16)
-    launch_rotary<__half>(p, split, norm, grid, s);
-  else
-    launch_rotary<float>(p, split, norm, grid, s);
-  return launch_status();
+  if (dtype == FQA_DTYPE_BF16) return launch_rotary<__nv_bfloat16>(p, split, norm, grid, s);
+  if (dtype == FQA_DTYPE_F16) return launch_rotary<__half>(p, split, norm, grid, s);
+  return launch_rotary<float>(p, split, norm, grid, s);
 }
 
 fqa_status fqa_e2m1_encode(const float* x, uint8_t* out, size_t npairs, void* cuda_stream) {

@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     mbar_init(done, 1);
     *abort_flag = 0;
     mbar_fence_init();
+    grid_wait();
     // the ring's first fill needs nothing else of the CTA
     for (int s = s0; s < min(s1, s0 + T::kStages); ++s) load_stage(s, s - s0);
   }
@@ -217,8 +218,10 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     tmem_alloc(tmem_slot, T::kCols);
     tmem_relinquish();
   }
+  grid_wait();
   tc_fence_before();
   __syncthreads();
+  grid_release();                    // (tensor memory is taken)
   if (ranks > 1) cluster_arrive();   // waited for before the first access to a peer
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -500,8 +503,10 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  grid_wait();
   tc_fence_before();
   __syncthreads();
+  grid_release();                    // (tensor memory is taken)
   cluster_arrive();
   cluster_wait();                // the peer's barriers are ready too
   tc_fence_after();

@@ -409,6 +409,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
   __shared__ float red_sum[TPR / 32];
   __shared__ uint32_t red_max[TPR / 32];
+  grid_release();
+  grid_wait();
   const int t = threadIdx.x % TPR;
   const int row = blockIdx.x * kRows + threadIdx.x / TPR;
   if (row >= p.M) return;                       // whole warps (and, for TPR >= 128, no CTA)
@@ -595,6 +597,8 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
   extern __shared__ __align__(16) float h[];   // Kw values, zeros past K
   __shared__ float red_sum[kMxAnyThreads / 32];
   __shared__ uint32_t red_max[kMxAnyThreads / 32];
+  grid_release();
+  grid_wait();
   const int t = threadIdx.x, row = blockIdx.x;
   const T* x = static_cast<const T*>(p.x) + (int64_t)row * p.ldx;
   const int chunks = p.KT * MxTraits<FMT>::kWordChunks, width = chunks * kMxChunk;
@@ -714,6 +718,8 @@ struct MxDequantParams {
 // side by side in a row and blockDim.y rows per CTA (no division per chunk).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParams p) {
+  grid_release();
+  grid_wait();
   constexpr int kBlock = MxTraits<FMT>::kBlock;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= p.M) return;
@@ -754,6 +760,8 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParam
 // so that a warp's stores are one segment.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantParams p) {
+  grid_release();
+  grid_wait();
   constexpr int kBlock = MxTraits<FMT>::kBlock;
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= p.M) return;
