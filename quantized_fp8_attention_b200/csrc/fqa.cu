@@ -272,15 +272,16 @@ static fqa_status launch_overlapped(void (*fn)(P...), dim3 grid, dim3 block, int
 
 // One launch of the row kernel that fits the row: 16 elements a thread and
 // chunk, two chunks in registers (one of binary32: 103 registers a thread left
-// two CTAs per SM, 23 us for 1023 x 5100).  Threads per row by its length: a
-// warp for short ones (no block-wide sums), then 128, 256 and 512; longer rows
-// are read again for each step.  Rows off the 16-byte boundaries go through
-// shared memory while they fit there.
+// two CTAs per SM, 23 us for 1023 x 5100).  A warp takes a row that fits it (no
+// CTA-wide sums); else a CTA of just the warps it needs (1023 x 5100 in 512
+// threads instead of 320: 19 us); rows beyond 512 threads are read again for
+// each step.  Rows off the 16-byte boundaries go through shared memory while
+// they fit there.
 template <typename T, int FMT, bool kNorm>
 static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s) {
   constexpr int NCH = sizeof(T) == 4 ? 1 : 2;
   const int chunks = p.KT * MxTraits<FMT>::kWordChunks;
-  const int threads = chunks / NCH;              // that hold the row's words, whole
+  const int threads = (chunks + NCH - 1) / NCH;  // that hold the row's words, whole
   if (!vec && chunks * kMxChunk <= kMxAnyCols) {
     const int smem = chunks * kMxChunk * 4;
     const auto fn = mx_row_any_kernel<T, FMT, kNorm>;
@@ -289,16 +290,13 @@ static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s)
       return FQA_ERR_CUDA;
     return launch_overlapped(fn, p.M, kMxAnyThreads, smem, s, 1, p);
   }
-  if (!vec) return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 512, 1, true, false>, p.M, 512, 0, s, 1, p);
+  if (!vec) return launch_overlapped(mx_row_kernel<T, FMT, kNorm, true, 1, true, false>, p.M, 512, 0, s, 1, p);
   if (threads <= 32)
-    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 32, NCH, false, true>, (p.M + 3) / 4, 128, 0, s, 1, p);
-  if (threads <= 128)
-    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 128, NCH, false, true>, p.M, 128, 0, s, 1, p);
-  if (threads <= 256)
-    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 256, NCH, false, true>, p.M, 256, 0, s, 1, p);
+    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, false, NCH, false, true>, (p.M + 3) / 4, 128, 0, s, 1, p);
   if (threads <= 512)
-    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 512, NCH, false, true>, p.M, 512, 0, s, 1, p);
-  return launch_overlapped(mx_row_kernel<T, FMT, kNorm, 512, 1, true, true>, p.M, 512, 0, s, 1, p);
+    return launch_overlapped(mx_row_kernel<T, FMT, kNorm, true, NCH, false, true>, p.M, (threads + 31) / 32 * 32, 0, s,
+                             1, p);
+  return launch_overlapped(mx_row_kernel<T, FMT, kNorm, true, 1, true, true>, p.M, 512, 0, s, 1, p);
 }
 
 template <typename T, bool kNorm>

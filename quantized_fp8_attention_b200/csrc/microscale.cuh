@@ -371,49 +371,50 @@ __device__ __forceinline__ void emit_chunk(const MxRowParams& p, uint8_t* codes,
   if (c % F::kWordChunks == 0 && word < p.KT) words[(size_t)word * 128] = w;
 }
 
-// Reductions over the TPR threads of a row (one warp, or the whole CTA).
-template <int TPR>
+// Reductions over the threads of a row: one warp, or the whole CTA (kCta, up to
+// 16 warps).
+template <bool kCta>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if constexpr (TPR > 32) {
+  if constexpr (kCta) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    v = lane < TPR / 32 ? red[lane] : 0.0f;
+    v = lane < (int)(blockDim.x >> 5) ? red[lane] : 0.0f;
 #pragma unroll
-    for (int o = TPR / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     v = __shfl_sync(0xFFFFFFFFu, v, 0);
   }
   return v;
 }
-template <int TPR>
+template <bool kCta>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   v = __reduce_max_sync(0xFFFFFFFFu, v);
-  if constexpr (TPR > 32) {
+  if constexpr (kCta) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    v = __reduce_max_sync(0xFFFFFFFFu, lane < TPR / 32 ? red[lane] : 0u);
+    v = __reduce_max_sync(0xFFFFFFFFu, lane < (int)(blockDim.x >> 5) ? red[lane] : 0u);
   }
   return v;
 }
 
-// One row per TPR threads, NCH chunks of 16 elements each held in registers
-// (kLoop: rows longer than TPR * NCH * 16, or not on vector boundaries, are
-// read again for each step instead).  Normed: h = x + residual in binary32,
+// One row per warp (four a CTA) or per CTA (kCta) of as many warps as its chunks
+// of 16 elements need, NCH a thread, held in registers; kLoop: a CTA's row too
+// long for that is read again for each step instead.  Normed: h = x + residual in binary32,
 // residual_out = h rounded, y = h / sqrt(mean h^2 + eps) * weight, and y is
 // quantized (never h's rounding: the norm sees the sum itself).
-template <typename T, int FMT, bool kNorm, int TPR, int NCH, bool kLoop, bool kVec>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxRowParams p) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  __shared__ float red_sum[TPR / 32];
-  __shared__ uint32_t red_max[TPR / 32];
+template <typename T, int FMT, bool kNorm, bool kCta, int NCH, bool kLoop, bool kVec>
+__global__ void __launch_bounds__(kCta ? 512 : 128) mx_row_kernel(const MxRowParams p) {
+  __shared__ float red_sum[16];
+  __shared__ uint32_t red_max[16];
   grid_release();
   grid_wait();
-  const int t = threadIdx.x % TPR;
-  const int row = blockIdx.x * kRows + threadIdx.x / TPR;
-  if (row >= p.M) return;                       // whole warps (and, for TPR >= 128, no CTA)
+  const int TPR = kCta ? blockDim.x : 32;        // threads per row
+  const int t = kCta ? threadIdx.x : threadIdx.x & 31;
+  const int row = kCta ? blockIdx.x : blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= p.M) return;                       // whole warps (and no CTA of a row's own)
   const T* x = static_cast<const T*>(p.x) + (int64_t)row * p.ldx;
   const bool res = kNorm && p.residual != nullptr;
   uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
         if (kMxChunk * c + e >= p.K) v[e] = 0.0f;
     }
   };
-  auto inverse_root = [&](float ss) { return __frsqrt_rn(__fdiv_rn(row_sum<TPR>(ss, red_sum), (float)p.K) + p.eps); };
+  auto inverse_root = [&](float ss) { return __frsqrt_rn(__fdiv_rn(row_sum<kCta>(ss, red_sum), (float)p.K) + p.eps); };
   auto store_row_scale = [&](uint32_t amax) {
     if (FMT == kNvFp4 && t == 0)
       p.row_scale[row] = __uint_as_float(
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
       amax[j] = chunk_amax(v[j]);
       top = max(top, amax[j]);
     }
-    if constexpr (FMT == kNvFp4) top = row_max<TPR>(top, red_max);
+    if constexpr (FMT == kNvFp4) top = row_max<kCta>(top, red_max);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) emit_chunk<FMT>(p, codes, words, t + j * TPR, v[j], amax[j], top);
     store_row_scale(top);
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) mx_row_kernel(const MxR
         if constexpr (kNorm) normed(t + i * TPR, rstd, v[0]);
         amax = max(amax, chunk_amax(v[0]));
       }
-      amax = row_max<TPR>(amax, red_max);
+      amax = row_max<kCta>(amax, red_max);
     }
     // residual_out may be residual itself: each thread writes an element only
     // here, after its own last read of it
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
   for (int e = p.K + t; e < width; e += kMxAnyThreads) h[e] = 0.0f;
   uint32_t top = 0;
   if constexpr (kNorm) {
-    const float rstd = __frsqrt_rn(__fdiv_rn(row_sum<kMxAnyThreads>(ss, red_sum), (float)p.K) + p.eps);
+    const float rstd = __frsqrt_rn(__fdiv_rn(row_sum<true>(ss, red_sum), (float)p.K) + p.eps);
     for (int e0 = t; e0 < p.K; e0 += B * kMxAnyThreads) {
       float w[B];
 #pragma unroll
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
   } else if constexpr (FMT == kNvFp4) {
     for (int e = t; e < p.K; e += kMxAnyThreads) top = max(top, __float_as_uint(h[e]) & 0x7FFFFFFFu);
   }
-  if constexpr (FMT == kNvFp4) top = row_max<kMxAnyThreads>(top, red_max);
+  if constexpr (FMT == kNvFp4) top = row_max<true>(top, red_max);
   __syncthreads();
   uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
   uint32_t* words = p.scales + (size_t)(row >> 7) * p.KT * 128 + (row & 31) * 4 + ((row >> 5) & 3);
