@@ -638,10 +638,15 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
           for (int e = 0; e < 32; e += 4) {
             const float4 f = *reinterpret_cast<const float4*>(rb + 32 * c + e);
             const float4 g = *reinterpret_cast<const float4*>(bias + 32 * c + e);
-            u[c][e] = __float_as_uint(fmaf(__uint_as_float(u[c][e]) * ra, f.x, g.x));
-            u[c][e + 1] = __float_as_uint(fmaf(__uint_as_float(u[c][e + 1]) * ra, f.y, g.y));
-            u[c][e + 2] = __float_as_uint(fmaf(__uint_as_float(u[c][e + 2]) * ra, f.z, g.z));
-            u[c][e + 3] = __float_as_uint(fmaf(__uint_as_float(u[c][e + 3]) * ra, f.w, g.w));
+            const float2 r2 = make_float2(ra, ra);
+            const float2 lo = f2_fma(f2_mul(make_float2(__uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1])), r2),
+                                     make_float2(f.x, f.y), make_float2(g.x, g.y));
+            const float2 hi = f2_fma(f2_mul(make_float2(__uint_as_float(u[c][e + 2]), __uint_as_float(u[c][e + 3])), r2),
+                                     make_float2(f.z, f.w), make_float2(g.z, g.w));
+            u[c][e] = __float_as_uint(lo.x);
+            u[c][e + 1] = __float_as_uint(lo.y);
+            u[c][e + 2] = __float_as_uint(hi.x);
+            u[c][e + 3] = __float_as_uint(hi.y);
           }
         }
       }
