@@ -585,14 +585,14 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
 def _elsewhere(index: int, stream, inputs):
     """None where a call is for the current device and stream.  Otherwise the
     context that makes them so: the tensors' device becomes current, and where a
-    stream is given outputs are allocated on it and the inputs marked as used
-    by it."""
+    stream is given outputs are allocated on it and the tensors given marked as
+    used by it."""
     if stream is None:
         return None if index == torch.cuda.current_device() else torch.cuda.device(index)
     if stream.device.index != index:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
     for t in inputs:
-        if t is not None:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(stream)
     return torch.cuda.stream(stream)
 
@@ -734,7 +734,7 @@ def mx_quantize(x: torch.Tensor, fmt: str, out: Optional[Microscaled] = None, st
     if out is None and stream is None and (q := (_native or _short_way()).quantize(x, fmt)) is not None:
         return q
     index = _device_tensor(x, "x")
-    if (there := _elsewhere(index, stream, (x,))) is not None:
+    if (there := _elsewhere(index, stream, (x, *(() if out is None else out[:3])))) is not None:
         with there:
             return mx_quantize(x, fmt, out)
     dtype, code = _float_dtype(x, "x"), _mx_format(fmt)
@@ -754,7 +754,7 @@ def mx_dequantize(q: Microscaled, out_dtype: int = FQA_OUT_BF16, out: Optional[t
     if out is None and stream is None and (v := (_native or _short_way()).dequantize(q, out_dtype)) is not None:
         return v
     M, code, index = _require_microscaled(q, "q")
-    if (there := _elsewhere(index, stream, q[:3])) is not None:
+    if (there := _elsewhere(index, stream, (*q[:3], out))) is not None:
         with there:
             return mx_dequantize(q, out_dtype, out)
     dt = _OUT_DTYPE.get(out_dtype)
@@ -782,7 +782,7 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, fmt: str = "mxfp8", resid
             y := (_native or _short_way()).rms_norm(x, weight, fmt, residual, eps)) is not None:
         return y
     index = _device_tensor(x, "x")
-    if (there := _elsewhere(index, stream, (x, weight, residual))) is not None:
+    if (there := _elsewhere(index, stream, (x, weight, residual, residual_out, *(() if out is None else out[:3])))) is not None:
         with there:
             return mx_rms_norm(x, weight, fmt, residual, eps, out, residual_out)
     dtype, code = _float_dtype(x, "x"), _mx_format(fmt)
@@ -828,7 +828,7 @@ def mx_matmul(a: Microscaled, b: Microscaled, bias: Optional[torch.Tensor] = Non
         return y
     M, code, index = _require_microscaled(a, "a")
     N, other, _ = _require_microscaled(b, "b", index)
-    if (there := _elsewhere(index, stream, (*a[:3], *b[:3], bias))) is not None:
+    if (there := _elsewhere(index, stream, (*a[:3], *b[:3], bias, out))) is not None:
         with there:
             return mx_matmul(a, b, bias, out_dtype, out)
     if other != code or a.cols != b.cols:
@@ -891,7 +891,7 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary, inverse: boo
     if not isinstance(rot, Rotary):
         raise TypeError(f"rot: expected a Rotary, got {type(rot).__name__}")
     pos, axes, theta, split, shared, q_weight, k_weight, eps = rot
-    if (there := _elsewhere(index, stream, (q, k, pos, q_weight, k_weight))) is not None:
+    if (there := _elsewhere(index, stream, (q, k, pos, q_weight, k_weight, q_out, k_out))) is not None:
         with there:
             return rotary(q, k, rot, inverse, q_out, k_out)
     dtype = _float_dtype(q, "q")

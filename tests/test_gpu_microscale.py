@@ -293,6 +293,7 @@ def test_refusals():
     for bad in (lambda: f.mx_quantize(x, "mxfp6"), lambda: f.mx_quantize(x, 0), lambda: f.mx_quantize(x[0], "mxfp8"),
                 lambda: f.mx_quantize(x.T, "mxfp8"), lambda: f.mx_quantize(x.int(), "mxfp8"),
                 lambda: f.mx_quantize(x[:, :0], "mxfp8"), lambda: f.mx_quantize(x, "mxfp4", out=q),
+                lambda: f.mx_quantize(x, "mxfp4", out=h), lambda: f.mx_rms_norm(x, w, out=h),
                 lambda: f.mx_quantize(x[:3], "nvfp4", out=q), lambda: f.mx_quantize(x[:, :32], "nvfp4", out=q),
                 lambda: f.mx_quantize(x, "mxfp4", out=m._replace(codes=x.view(torch.uint8)[:, :32])),
                 lambda: f.mx_quantize(x, "mxfp4", out=m._replace(codes=x.view(torch.uint8).flatten()[:128].view(4, 32))),
@@ -342,3 +343,27 @@ def test_the_short_way_and_the_checked_one_agree():
     assert b.quantize(x[0], "mxfp8") is None and b.quantize(x.T, "mxfp8") is None and b.quantize(x, "mxfp6") is None
     assert b.matmul(q, q, None, 0) is None and b.matmul(y, y, bias[:3], 0) is None
     assert b.rotate(q, k[:, :, :3], rot, False) is None and b.rotate(q, k, rot._replace(axes=[64, 64]), False) is None
+
+
+@pytest.mark.parametrize("K", [4096, 4097])
+def test_rows_beyond_two_to_the_31_elements(K):
+    """The last rows of 2.2e9 elements hold what they hold alone (both row paths)."""
+    f = fqa()
+    M = 128 * 4200 + 5
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    x[:200].normal_()
+    x[200:-200] = 0
+    x[-200:].normal_()
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    q = f.mx_quantize(x, "nvfp4")
+    tail = f.mx_quantize(x[-133:].contiguous(), "nvfp4")
+    assert torch.equal(q.codes[-133:], tail.codes) and torch.equal(q.row_scale[-133:], tail.row_scale)
+    # row M - 133 starts a block of 128 rows, so the tiles line up (rows past M are not written)
+    last, want = R.untile(q.scales[-2:], 133, 4), R.untile(tail.scales, 133, 4)
+    assert np.array_equal(last, want)
+    v = f.mx_dequantize(q)
+    assert torch.equal(v[-133:], f.mx_dequantize(tail))
+    del v
+    y, h = f.mx_rms_norm(x, w, "mxfp8", residual=x)
+    y2, h2 = f.mx_rms_norm(x[-133:].contiguous(), w, "mxfp8", residual=x[-133:].contiguous())
+    assert torch.equal(y.codes[-133:], y2.codes) and torch.equal(h[-133:], h2)

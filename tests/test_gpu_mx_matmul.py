@@ -70,7 +70,8 @@ def test_few_rows(fmt, M, N, K):
 @pytest.mark.parametrize("fmt", R.FORMATS)
 @pytest.mark.parametrize("M,N,K", [
     (256, 256, 32), (257, 511, 96), (300, 1000, 480), (513, 768, 1024), (1024, 4096, 256), (1000, 2056, 4096),
-    (2048, 2304, 544), (4608, 1536, 1120), (3001, 2049, 64), (700, 8200, 33)])
+    (2048, 2304, 544), (4608, 1536, 1120), (3001, 2049, 64), (700, 8200, 33), (19000, 16, 64), (19100, 8, 96),
+    (19001, 1, 32), (20000, 40, 288), (2500, 2304, 20000), (4000, 1282, 4128)])
 def test_many_rows(fmt, M, N, K):
     check(M, N, K, fmt, bias=N % 2 == 0, seed=M + N + K)
 
@@ -83,7 +84,7 @@ def test_output_types(fmt, out_dtype, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", R.FORMATS)
-@pytest.mark.parametrize("M", [3, 70, 1100])
+@pytest.mark.parametrize("M", [3, 70, 1100, 3000])
 def test_single_products_land_where_they_belong(fmt, M):
     """A's row m is one value at channel (7 m) % K, so every result is that value
     times one code of B: exact, and any misplaced row, channel or scale shows.
@@ -100,7 +101,7 @@ def test_single_products_land_where_they_belong(fmt, M):
 
 
 @pytest.mark.parametrize("fmt", R.FORMATS)
-@pytest.mark.parametrize("M,N", [(5, 300), (1200, 1100)])
+@pytest.mark.parametrize("M,N", [(5, 300), (1200, 1100), (2600, 1300)])
 def test_rows_that_stand_for_nan(fmt, M, N):
     """NaN in A's row m or B's row n spoils that row or column of the result only."""
     f = fqa()
@@ -121,7 +122,7 @@ def test_empty_sides():
         assert f.mx_matmul(e, a).shape == (0, 5) and f.mx_matmul(a, e).shape == (5, 0)
 
 
-@pytest.mark.parametrize("M", [1, 100, 1500])
+@pytest.mark.parametrize("M", [1, 100, 1500, 3000])
 def test_the_same_call_gives_the_same_bits(M):
     f = fqa()
     a, b = R.random_microscaled(M, 4096, "nvfp4", 1), R.random_microscaled(1030, 4096, "nvfp4", 2)
@@ -132,7 +133,7 @@ def test_the_same_call_gives_the_same_bits(M):
 
 def test_two_streams_at_once_and_replayed_graphs():
     f = fqa()
-    sizes = ((1, 4096, 4096), (100, 1000, 2048), (1300, 1500, 1024))
+    sizes = ((1, 4096, 4096), (100, 1000, 2048), (2500, 1500, 1024))
     ops = [(R.random_microscaled(M, K, "nvfp4", 1), R.random_microscaled(N, K, "nvfp4", 2)) for M, N, K in sizes]
     want = [f.mx_matmul(a, b) for a, b in ops]
     torch.cuda.synchronize()
@@ -187,3 +188,67 @@ def test_a_block_up_to_its_attention(fmt):
     rel = (out.double() - want).norm() / want.norm()
     assert rel < 4 * 2.0 ** -4
     assert f.fqa_debug_status()[0] == f.FQA_OK
+
+
+def test_every_row_count_around_the_tiles():
+    """1 to 300 rows against one set of weights: each row is the row that the
+    whole product has (the split of K, and with it the sum's order, may differ
+    with the row count, so to the sums' rounding)."""
+    f = fqa()
+    K, N = 2080, 200
+    a, b = R.random_microscaled(300, K, "nvfp4", 1, wide=True), R.random_microscaled(N, K, "nvfp4", 2, wide=True)
+    y, mag = reference(a, b, None)
+    lim = bound(y, mag, K, torch.float32)
+    x = f.mx_dequantize(a, 1)
+    for M in (1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300):
+        part = f.Microscaled(a.codes[:M].contiguous(), a.scales[: -(-M // 128)].contiguous(),
+                             a.row_scale[:M].contiguous(), K, "nvfp4")
+        err = (f.mx_matmul(part, b, out_dtype=1).double() - y[:M]).abs()
+        assert (err <= lim[:M]).all(), M
+    assert x.shape == (300, K)
+
+
+def test_a_chain_without_waiting():
+    """Norm, product, quantization, product and the way back over the same
+    buffers again and again, nothing waited for: launches overlap with the end of
+    the one before, and have to give what they give one at a time."""
+    f = fqa()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    M, K, N = 500, 1024, 768
+    x = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    up = f.mx_quantize(torch.randn(N, K, device="cuda", generator=g).bfloat16() / 32, "nvfp4")
+    down = f.mx_quantize(torch.randn(K, N, device="cuda", generator=g).bfloat16() / 28, "nvfp4")
+
+    def run(wait):
+        h = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+        step = x.clone()
+        q, m = f.alloc_microscaled(M, K, "nvfp4", "cuda"), f.alloc_microscaled(M, N, "nvfp4", "cuda")
+        mid = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        for _ in range(60):
+            f.mx_rms_norm(step, w, "nvfp4", residual=h, residual_out=h, out=q)
+            if wait:
+                torch.cuda.synchronize()
+            f.mx_matmul(q, up, out=mid)
+            if wait:
+                torch.cuda.synchronize()
+            f.mx_quantize(mid, "nvfp4", out=m)
+            if wait:
+                torch.cuda.synchronize()
+            f.mx_matmul(m, down, out=step)
+            if wait:
+                torch.cuda.synchronize()
+        return h.clone(), step.clone()
+    want, got = run(True), run(False)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1]) and torch.isfinite(want[0]).all()
+
+
+def test_results_beyond_two_to_the_31():
+    f = fqa()
+    M, N = 70001, 32000                       # 2.24e9 results
+    a, b = R.random_microscaled(M, 32, "mxfp8", 1), R.random_microscaled(N, 32, "mxfp8", 2)
+    y = f.mx_matmul(a, b)
+    last = f.Microscaled(a.codes[-113:].contiguous(), a.scales[-1:].contiguous(), None, 32, "mxfp8")
+    assert M - 113 == a.scales[:-1].shape[0] * 128
+    assert torch.equal(y[-113:], f.mx_matmul(last, b))
+    assert torch.equal(y[:128], f.mx_matmul(f.Microscaled(a.codes[:128], a.scales[:1], None, 32, "mxfp8"), b))

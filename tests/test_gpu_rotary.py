@@ -214,3 +214,16 @@ def test_refusals():
     out = torch.empty_like(q)
     with pytest.raises(ValueError, match="overlaps"):
         f.rotary(q, q.clone(), rot, q_out=out, k_out=out)
+
+
+def test_rows_beyond_two_to_the_31_elements():
+    f = fqa()
+    N, H = 360_000, 48                        # 2.2e9 elements
+    packed = torch.empty(1, N, H, 128, dtype=torch.bfloat16, device="cuda")
+    packed[:, -50:].normal_()
+    q = packed.transpose(1, 2)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")[:, None]
+    rot = f.Rotary(pos, (128,))
+    y, _ = f.rotary(q, None, rot)
+    want, _ = f.rotary(q[:, :, -50:], None, rot._replace(positions=pos[-50:].contiguous()))
+    assert torch.equal(y[:, :, -50:], want)
