@@ -14,8 +14,8 @@
 //          saturates); s = E4M3(fl32(amax 2^-e / 6)); code = E2M1(x 2^-e / s),
 //          0 where s is 0.  A power of two keeps x 2^-e and every tie of 16-bit
 //          inputs exact, so the codes are those of exact arithmetic.
-// The quotient by s is x hi + x lo with hi = 1 / s in binary32 and lo the rest
-// of 1 / s: one multiply and one FMA instead of a division per element, right on
+// The quotient by s is x hi + x lo with hi just below 1 / s and lo the rest of
+// 1 / s: one multiply and one FMA instead of a division per element, right on
 // every tie (a tie is a product of s with a multiple of 1/4).
 // Non-finite values: an mx block that holds one gets the scale 0xFF (NaN) and
 // zero codes, an nvfp4 row gets a NaN row scale, zero scales and codes.
@@ -301,6 +301,21 @@ __device__ __forceinline__ void chunk_mul2(float (&v)[kMxChunk], float a, float 
   }
 }
 
+// x / 6 rounded to nearest, as x h + x l with h + l = 1/6 to 48 bits: off from
+// the quotient by 2^-47 of it, while a quotient by 6 that is not a binary32
+// value lies at least a sixth of a unit from the midpoint of two.
+__device__ __forceinline__ float sixth(float x) {
+  constexpr float h = 0x1.555556p-3f, l = -0x1.555556p-28f;
+  return __fmaf_rn(x, h, __fmul_rn(x, l));
+}
+
+// A value one to three units below 1 / s (inf for 0).
+__device__ __forceinline__ float below_reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));   // off by at most one unit
+  return __uint_as_float(__float_as_uint(r) - 2u);
+}
+
 struct MxRowParams {
   const void* x;          // [M] rows of K, row stride ldx (elements)
   const void* residual;   // the same shape, row stride ldr; binary32 if res_f32, else x's type
@@ -332,10 +347,10 @@ __device__ __forceinline__ void emit_chunk(const MxRowParams& p, uint8_t* codes,
     if (row_amax < 0x7F800000u) {
       const int e = power_byte(row_amax, 11, 0x280000u, 1);
       const float inv = inverse_power(e);
-      byte = e4m3x2(__fdiv_rn(__uint_as_float(amax) * inv, 6.0f), 0.0f) & 0xFFu;
+      byte = e4m3x2(sixth(__uint_as_float(amax) * inv), 0.0f) & 0xFFu;
       const float s = e4m3x2_to_f2(byte).x;
-      float hi = __frcp_rz(s);         // rounded down: lo >= 0, so a zero keeps its sign below
-      float lo = __fmul_rn(__fmaf_rn(-s, hi, 1.0f), hi);
+      float hi = below_reciprocal(s);
+      float lo = __fmul_rn(__fmaf_rn(-s, hi, 1.0f), hi);   // >= 0, so a zero keeps its sign below
       if (e >= 27 && e <= 207) {       // the row's power goes into both parts, exactly
         hi *= inv;
         lo *= inv;
@@ -409,8 +424,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
 // Bound by memory: every input is read once, all loads of a row are in flight
 // before its first sum, in 32-byte accesses.  8704 x 4096 BF16 with residual to
 // mxfp8 moves 251 MB in 39 us (6.4 TB/s, 98% of a copy's rate), 12288 x 4096 BF16
-// to nvfp4 129 MB in 26 us (the longest of the three: two roundings of scales,
-// two products per element; mxfp8 153 MB in 24 us).
+// to nvfp4 129 MB in 24 us (two roundings of scales and two products per element;
+// mxfp8 153 MB in 24 us).
 template <typename T, int FMT, bool kNorm, bool kCta, int NCH, bool kLoop, bool kVec>
 __global__ void __launch_bounds__(kCta ? 512 : 128) mx_row_kernel(const MxRowParams p) {
   __shared__ float red_sum[16];
