@@ -27,6 +27,7 @@
 #pragma once
 
 #include "device.cuh"
+#include "launch.cuh"
 
 namespace fqa {
 
