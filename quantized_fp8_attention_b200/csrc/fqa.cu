@@ -315,11 +315,15 @@ static fqa_status launch_mx(const MxRowParams& p, int dtype, int fmt, bool vec, 
 
 template <typename T, int FMT>
 static fqa_status launch_mx_dequantize(const MxDequantParams& p, bool vec, cudaStream_t s) {
-  const int items = (p.K + (vec ? kMxChunk : 2) - 1) / (vec ? kMxChunk : 2);
+  const bool four = !vec && sizeof(T) == 2 && p.K % 4 == 0 && aligned(p.out, 8);
+  const int width = vec ? kMxChunk : four ? 4 : 2, items = (p.K + width - 1) / width;
   int tx = 4;                            // items side by side: a power of two, up to a whole CTA
   while (tx < items && tx < 256) tx *= 2;
   const dim3 block(tx, 256 / tx), grid((p.M + block.y - 1) / block.y);
-  return launch_overlapped(vec ? mx_dequantize_kernel<T, FMT> : mx_dequantize_any_kernel<T, FMT>, grid, block, 0, s, 1, p);
+  if (vec) return launch_overlapped(mx_dequantize_kernel<T, FMT>, grid, block, 0, s, 1, p);
+  if constexpr (sizeof(T) == 2)
+    if (four) return launch_overlapped(mx_dequantize_any_kernel<T, FMT, 4>, grid, block, 0, s, 1, p);
+  return launch_overlapped(mx_dequantize_any_kernel<T, FMT, 2>, grid, block, 0, s, 1, p);
 }
 
 template <typename T>

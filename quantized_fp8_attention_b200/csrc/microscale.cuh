@@ -781,9 +781,10 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParam
   }
 }
 
-// The same for rows off the 16-byte boundaries: a thread takes two neighbours,
-// so that a warp's stores are one segment.
-template <typename T, int FMT>
+// The same for rows off the 16-byte boundaries: a thread takes W neighbours, so
+// that a warp's stores are one segment: four (16-bit rows on 8-byte boundaries),
+// or two, stored one by one.
+template <typename T, int FMT, int W>
 __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantParams p) {
   grid_release();
   grid_wait();
@@ -795,14 +796,24 @@ __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantP
   const float rs = FMT == kNvFp4 ? __ldg(p.row_scale + row) : 1.0f;
   T* out = static_cast<T*>(p.out) + (int64_t)row * p.K;
 #pragma unroll 4
-  for (int c = threadIdx.x; 2 * c < p.K; c += blockDim.x) {
-    const int blk = 2 * c / kBlock;
+  for (int c = threadIdx.x; W * c < p.K; c += blockDim.x) {
+    const int blk = W * c / kBlock;
     const uint32_t sb = sf[(size_t)(blk >> 2) * 512 + (blk & 3)];
-    const float2 f = FMT == kMxFp8 ? e4m3x2_to_f2(*reinterpret_cast<const uint16_t*>(codes + 2 * (size_t)c))
-                                   : e2m1x2_to_f2(codes[c]);
     const float s = FMT == kNvFp4 ? e4m3x2_to_f2(sb).x : e8m0_to_f32(sb);
-    out[2 * c] = from_f32<T>(FMT == kNvFp4 ? f.x * s * rs : f.x * s);
-    if (2 * c + 1 < p.K) out[2 * c + 1] = from_f32<T>(FMT == kNvFp4 ? f.y * s * rs : f.y * s);
+    float v[W];
+#pragma unroll
+    for (int e = 0; e < W; e += 2) {
+      const float2 f = FMT == kMxFp8 ? e4m3x2_to_f2(*reinterpret_cast<const uint16_t*>(codes + W * (size_t)c + e))
+                                     : e2m1x2_to_f2(codes[(W * (size_t)c + e) / 2]);
+      v[e] = FMT == kNvFp4 ? f.x * s * rs : f.x * s;
+      v[e + 1] = FMT == kNvFp4 ? f.y * s * rs : f.y * s;
+    }
+    if constexpr (W == 4) {
+      store_vec<T, 4>(out + 4 * c, v);
+    } else {
+      out[2 * c] = from_f32<T>(v[0]);
+      if (2 * c + 1 < p.K) out[2 * c + 1] = from_f32<T>(v[1]);
+    }
   }
 }
 
