@@ -278,13 +278,13 @@ static fqa_status launch_overlapped(void (*fn)(P...), dim3 grid, dim3 block, int
 // each step.  Rows off the 16-byte boundaries go through shared memory while
 // they fit there.
 template <typename T, int FMT, bool kNorm>
-static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s) {
+static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, bool pairs, cudaStream_t s) {
   constexpr int NCH = sizeof(T) == 4 ? 1 : 2;
   const int chunks = p.KT * MxTraits<FMT>::kWordChunks;
   const int threads = (chunks + NCH - 1) / NCH;  // that hold the row's words, whole
   if (!vec && chunks * kMxChunk <= kMxAnyCols) {
     const int smem = chunks * kMxChunk * 4;
-    const auto fn = mx_row_any_kernel<T, FMT, kNorm>;
+    const auto fn = pairs ? mx_row_any_kernel<T, FMT, kNorm, 2> : mx_row_any_kernel<T, FMT, kNorm, 1>;
     if (smem > 48 * 1024 && cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  kMxAnyCols * 4) != cudaSuccess)
       return FQA_ERR_CUDA;
@@ -300,17 +300,20 @@ static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, cudaStream_t s)
 }
 
 template <typename T, bool kNorm>
-static fqa_status launch_mx_format(const MxRowParams& p, int fmt, bool vec, cudaStream_t s) {
-  if (fmt == FQA_MXFP8) return launch_mx_rows<T, kMxFp8, kNorm>(p, vec, s);
-  if (fmt == FQA_MXFP4) return launch_mx_rows<T, kMxFp4, kNorm>(p, vec, s);
-  return launch_mx_rows<T, kNvFp4, kNorm>(p, vec, s);
+static fqa_status launch_mx_format(const MxRowParams& p, int fmt, bool vec, bool pairs, cudaStream_t s) {
+  if (fmt == FQA_MXFP8) return launch_mx_rows<T, kMxFp8, kNorm>(p, vec, pairs, s);
+  if (fmt == FQA_MXFP4) return launch_mx_rows<T, kMxFp4, kNorm>(p, vec, pairs, s);
+  return launch_mx_rows<T, kNvFp4, kNorm>(p, vec, pairs, s);
 }
 
+// align: the widest access that every row of every tensor allows, of 32, 16, 2
+// values or 1 (see rows_vectorize()).
 template <bool kNorm>
-static fqa_status launch_mx(const MxRowParams& p, int dtype, int fmt, bool vec, cudaStream_t s) {
-  if (dtype == FQA_DTYPE_BF16) return launch_mx_format<__nv_bfloat16, kNorm>(p, fmt, vec, s);
-  if (dtype == FQA_DTYPE_F16) return launch_mx_format<__half, kNorm>(p, fmt, vec, s);
-  return launch_mx_format<float, kNorm>(p, fmt, vec, s);
+static fqa_status launch_mx(const MxRowParams& p, int dtype, int fmt, int align, cudaStream_t s) {
+  const bool vec = align >= 16, pairs = align >= 2;
+  if (dtype == FQA_DTYPE_BF16) return launch_mx_format<__nv_bfloat16, kNorm>(p, fmt, vec, pairs, s);
+  if (dtype == FQA_DTYPE_F16) return launch_mx_format<__half, kNorm>(p, fmt, vec, pairs, s);
+  return launch_mx_format<float, kNorm>(p, fmt, vec, pairs, s);
 }
 
 template <typename T, int FMT>
@@ -807,12 +810,12 @@ size_t fqa_mx_scale_bytes(int M, int K, fqa_mx_format fmt) {
   return (size_t)((M + 127) / 128) * mx_words(K, fmt) * 512;
 }
 
-// The widest access, 32 or 16 bytes (or 0), that every row's start and length
-// are multiples of.
+// The widest access that every row's start and length are multiples of: 32 or
+// 16 bytes, or two elements (2), or one (1).
 static int rows_vectorize(const void* base, int64_t ld, int K, size_t elt) {
-  for (int w : {32, 16})
-    if (K * elt % w == 0 && aligned(base, w) && (ld * (int64_t)elt) % w == 0) return w;
-  return 0;
+  for (size_t w : {(size_t)32, (size_t)16, 2 * elt})
+    if (K * elt % w == 0 && aligned(base, w) && (ld * (int64_t)elt) % (int64_t)w == 0) return w == 2 * elt ? 2 : (int)w;
+  return 1;
 }
 
 // The checks and fields common to both row calls.
@@ -846,7 +849,7 @@ fqa_status fqa_mx_quantize(const void* x, fqa_dtype dtype, int M, int K, int64_t
   if (st != FQA_OK || M == 0) return st;
   const int vec = rows_vectorize(x, ldx, K, dtype_bytes(dtype));
   p.wide = vec == 32;
-  return launch_mx<false>(p, dtype, fmt, vec != 0, static_cast<cudaStream_t>(cuda_stream));
+  return launch_mx<false>(p, dtype, fmt, vec, static_cast<cudaStream_t>(cuda_stream));
 }
 
 fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t ldx, const void* weight,
@@ -877,7 +880,7 @@ fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t
     vec = std::min({vec, rows_vectorize(residual, ldr, K, relt), rows_vectorize(residual_out, K, K, relt)});
   }
   p.wide = vec == 32;
-  return launch_mx<true>(p, dtype, fmt, vec != 0, static_cast<cudaStream_t>(cuda_stream));
+  return launch_mx<true>(p, dtype, fmt, vec, static_cast<cudaStream_t>(cuda_stream));
 }
 
 fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int M, int K,
@@ -890,11 +893,11 @@ fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const 
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(row_scale, 4) || !aligned(out, dtype_bytes(out_dtype)))
     return FQA_ERR_MISALIGNED;
   const int vec = rows_vectorize(out, K, K, dtype_bytes(out_dtype));
-  const MxDequantParams p{codes, scales, row_scale, out, M, K, mx_padded(K), mx_words(K, fmt), vec == 32};
+  const MxDequantParams p{codes, scales, row_scale, out, M, K, mx_padded(K), mx_words(K, fmt), vec == 32 || vec == 2};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  if (out_dtype == FQA_DTYPE_BF16) return launch_mx_dequantize_format<__nv_bfloat16>(p, fmt, vec != 0, s);
-  if (out_dtype == FQA_DTYPE_F16) return launch_mx_dequantize_format<__half>(p, fmt, vec != 0, s);
-  return launch_mx_dequantize_format<float>(p, fmt, vec != 0, s);
+  if (out_dtype == FQA_DTYPE_BF16) return launch_mx_dequantize_format<__nv_bfloat16>(p, fmt, vec >= 16, s);
+  if (out_dtype == FQA_DTYPE_F16) return launch_mx_dequantize_format<__half>(p, fmt, vec >= 16, s);
+  return launch_mx_dequantize_format<float>(p, fmt, vec >= 16, s);
 }
 
 fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,

@@ -26,6 +26,8 @@
 // aligned word; the words of a row are written whole, blocks past Kp as 0.
 #pragma once
 
+#include <type_traits>
+
 #include "device.cuh"
 #include "launch.cuh"
 
@@ -611,14 +613,43 @@ __global__ void __launch_bounds__(kCta ? 512 : 128) mx_row_kernel(const MxRowPar
 // row per CTA, read element by element along the row, so that a warp's loads and
 // stores are one segment, into shared memory as binary32; the chunks are taken
 // from there.  (Chunks of 16 straight from memory, element by element, touch a
-// sector per lane and load, and needed the row again for every step.)  8704 x 4097
-// BF16 with residual: 91 us, 2.8 TB/s, bound by its 2-byte accesses.
+// sector per lane and load, and needed the row again for every step: 156 us for
+// the norm of 8704 x 4097 BF16.)  Now 82 us there, 3.1 TB/s, bound by its 2-byte
+// accesses, and 70 us at 8704 x 4098 in pairs.
 constexpr int kMxAnyThreads = 256;
 constexpr int kMxAnyCols = 49152;            // longest row held
 
-template <typename T, int FMT, bool kNorm>
+// E neighbours (E * sizeof(T) bytes aligned) as binary32, and back.
+template <typename T, int E>
+struct MxFew {
+  std::conditional_t<E == 1, T, std::conditional_t<sizeof(T) == 4, uint2, uint32_t>> raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const decltype(raw)*>(p); }
+  __device__ __forceinline__ void get(float (&v)[E]) const {
+    if constexpr (E == 1) {
+      v[0] = to_f32<T>(raw);
+    } else if constexpr (sizeof(T) == 4) {
+      v[0] = __uint_as_float(raw.x);
+      v[1] = __uint_as_float(raw.y);
+    } else {
+      const float2 f = unpack2<T>(raw);
+      v[0] = f.x;
+      v[1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[E]) {
+    if constexpr (E == 1)
+      *p = from_f32<T>(v[0]);
+    else if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    else
+      *reinterpret_cast<uint32_t*>(p) = pack2<T>(v[0], v[1]);
+  }
+};
+
+// E: values per access, two where all rows allow it.
+template <typename T, int FMT, bool kNorm, int E>
 __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowParams p) {
-  extern __shared__ __align__(16) float h[];   // Kw values, zeros past K
+  extern __shared__ __align__(16) float h[];   // the row's values, zeros past K
   __shared__ float red_sum[kMxAnyThreads / 32];
   __shared__ uint32_t red_max[kMxAnyThreads / 32];
   grid_release();
@@ -628,71 +659,83 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
   const int chunks = p.KT * MxTraits<FMT>::kWordChunks, width = chunks * kMxChunk;
   const bool res = kNorm && p.residual != nullptr;
   float ss = 0.0f;
-  constexpr int B = 8;                           // elements a thread has in flight
-  for (int e0 = t; e0 < p.K; e0 += B * kMxAnyThreads) {
-    T a[B];
-    float r[B];
+  constexpr int B = 8, S = E * kMxAnyThreads;    // accesses a thread has in flight, and the step between them
+  // residual types: its row's pointers are formed where its type is known
+  auto pass = [&](auto type) {
+    using R = decltype(type);
+    const R* r = static_cast<const R*>(p.residual) + (int64_t)row * p.ldr;
+    R* ro = static_cast<R*>(p.residual_out) + (int64_t)row * p.K;
+    for (int e0 = E * t; e0 < p.K; e0 += B * S) {
+      MxFew<T, E> a[B];
+      MxFew<R, E> q[B];
 #pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int e = e0 + i * kMxAnyThreads;
-      a[i] = e < p.K ? x[e] : from_f32<T>(0.0f);
-    }
-    if (res && p.res_f32) {
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int e = e0 + i * kMxAnyThreads;
-        r[i] = e < p.K ? static_cast<const float*>(p.residual)[(int64_t)row * p.ldr + e] : 0.0f;
-      }
-    } else if (res) {
-      T q[B];
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int e = e0 + i * kMxAnyThreads;
-        q[i] = e < p.K ? static_cast<const T*>(p.residual)[(int64_t)row * p.ldr + e] : from_f32<T>(0.0f);
-      }
-#pragma unroll
-      for (int i = 0; i < B; ++i) r[i] = to_f32<T>(q[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      const int e = e0 + i * kMxAnyThreads;
-      if (e >= p.K) break;
-      float v = to_f32<T>(a[i]);
+      for (int i = 0; i < B; ++i)
+        if (e0 + i * S < p.K) a[i].load(x + e0 + i * S);
       if (res) {
-        v += r[i];
-        if (p.res_f32)
-          static_cast<float*>(p.residual_out)[(int64_t)row * p.K + e] = v;
-        else
-          static_cast<T*>(p.residual_out)[(int64_t)row * p.K + e] = from_f32<T>(v);
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+          if (e0 + i * S < p.K) q[i].load(r + e0 + i * S);
       }
-      h[e] = v;
-      if constexpr (kNorm) ss = fmaf(v, v, ss);
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int e = e0 + i * S;
+        if (e >= p.K) break;
+        float v[E];
+        a[i].get(v);
+        if (res) {
+          float w[E];
+          q[i].get(w);
+#pragma unroll
+          for (int k = 0; k < E; ++k) v[k] += w[k];
+          MxFew<R, E>::store(ro + e, v);
+        }
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          h[e + k] = v[k];
+          if constexpr (kNorm) ss = fmaf(v[k], v[k], ss);
+        }
+      }
     }
-  }
+  };
+  if (kNorm && p.res_f32)
+    pass(float{});
+  else
+    pass(T{});
   for (int e = p.K + t; e < width; e += kMxAnyThreads) h[e] = 0.0f;
   uint32_t top = 0;
   if constexpr (kNorm) {
     const float rstd = __frsqrt_rn(__fdiv_rn(row_sum<true>(ss, red_sum), (float)p.K) + p.eps);
-    for (int e0 = t; e0 < p.K; e0 += B * kMxAnyThreads) {
-      float w[B];
+    auto scale = [&](auto type) {
+      using W = decltype(type);
+      const W* wp = static_cast<const W*>(p.weight);
+      for (int e0 = E * t; e0 < p.K; e0 += B * S) {
+        MxFew<W, E> w[B];
 #pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int e = e0 + i * kMxAnyThreads;
-        w[i] = 0.0f;
-        if (e < p.K)
-          w[i] = p.w_f32 ? static_cast<const float*>(p.weight)[e] : to_f32<T>(static_cast<const T*>(p.weight)[e]);
-      }
+        for (int i = 0; i < B; ++i)
+          if (e0 + i * S < p.K) w[i].load(wp + e0 + i * S);
 #pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int e = e0 + i * kMxAnyThreads;
-        if (e >= p.K) break;
-        const float y = __fmul_rn(__fmul_rn(h[e], rstd), w[i]);
-        h[e] = y;
-        if constexpr (FMT == kNvFp4) top = max(top, __float_as_uint(y) & 0x7FFFFFFFu);
+        for (int i = 0; i < B; ++i) {
+          const int e = e0 + i * S;
+          if (e >= p.K) break;
+          float f[E];
+          w[i].get(f);
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            const float y = __fmul_rn(__fmul_rn(h[e + k], rstd), f[k]);
+            h[e + k] = y;
+            if constexpr (FMT == kNvFp4) top = max(top, __float_as_uint(y) & 0x7FFFFFFFu);
+          }
+        }
       }
-    }
+    };
+    if (p.w_f32)
+      scale(float{});
+    else
+      scale(T{});
   } else if constexpr (FMT == kNvFp4) {
-    for (int e = t; e < p.K; e += kMxAnyThreads) top = max(top, __float_as_uint(h[e]) & 0x7FFFFFFFu);
+    for (int e0 = E * t; e0 < p.K; e0 += S)      // this thread's own
+#pragma unroll
+      for (int k = 0; k < E; ++k) top = max(top, __float_as_uint(h[e0 + k]) & 0x7FFFFFFFu);
   }
   if constexpr (FMT == kNvFp4) top = row_max<true>(top, red_max);
   __syncthreads();
@@ -734,7 +777,7 @@ struct MxDequantParams {
   const float* row_scale;
   void* out;              // contiguous [M, K]
   int M, K, Kp, KT;
-  int wide;               // as MxRowParams
+  int wide;               // as MxRowParams (or, off 16-byte boundaries, rows on boundaries of two values)
 };
 
 // value = element * scale (exact in binary32) * row scale, rounded once more to
@@ -783,7 +826,7 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParam
 
 // The same for rows off the 16-byte boundaries: a thread takes W neighbours, so
 // that a warp's stores are one segment: four (16-bit rows on 8-byte boundaries),
-// or two, stored one by one.
+// or two, stored together where rows start on their boundaries (wide).
 template <typename T, int FMT, int W>
 __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantParams p) {
   grid_release();
@@ -810,6 +853,8 @@ __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantP
     }
     if constexpr (W == 4) {
       store_vec<T, 4>(out + 4 * c, v);
+    } else if (p.wide) {
+      MxFew<T, 2>::store(out + 2 * c, v);
     } else {
       out[2 * c] = from_f32<T>(v[0]);
       if (2 * c + 1 < p.K) out[2 * c + 1] = from_f32<T>(v[1]);
