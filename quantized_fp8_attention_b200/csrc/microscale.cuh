@@ -838,26 +838,41 @@ __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantP
   const uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
   const float rs = FMT == kNvFp4 ? __ldg(p.row_scale + row) : 1.0f;
   T* out = static_cast<T*>(p.out) + (int64_t)row * p.K;
-#pragma unroll 4
-  for (int c = threadIdx.x; W * c < p.K; c += blockDim.x) {
-    const int blk = W * c / kBlock;
-    const uint32_t sb = sf[(size_t)(blk >> 2) * 512 + (blk & 3)];
-    const float s = FMT == kNvFp4 ? e4m3x2_to_f2(sb).x : e8m0_to_f32(sb);
-    float v[W];
+  constexpr int B = 4;                           // groups a thread has in flight
+  for (int c0 = threadIdx.x; W * c0 < p.K; c0 += B * blockDim.x) {
+    uint32_t sb[B];
+    uint16_t code[B][W / 2];
 #pragma unroll
-    for (int e = 0; e < W; e += 2) {
-      const float2 f = FMT == kMxFp8 ? e4m3x2_to_f2(*reinterpret_cast<const uint16_t*>(codes + W * (size_t)c + e))
-                                     : e2m1x2_to_f2(codes[(W * (size_t)c + e) / 2]);
-      v[e] = FMT == kNvFp4 ? f.x * s * rs : f.x * s;
-      v[e + 1] = FMT == kNvFp4 ? f.y * s * rs : f.y * s;
+    for (int i = 0; i < B; ++i) {
+      const int c = c0 + i * (int)blockDim.x;
+      if (W * c >= p.K) break;
+      const int blk = W * c / kBlock;
+      sb[i] = sf[(size_t)(blk >> 2) * 512 + (blk & 3)];
+#pragma unroll
+      for (int e = 0; e < W / 2; ++e)
+        code[i][e] = FMT == kMxFp8 ? *reinterpret_cast<const uint16_t*>(codes + W * (size_t)c + 2 * e)
+                                   : codes[W / 2 * (size_t)c + e];
     }
-    if constexpr (W == 4) {
-      store_vec<T, 4>(out + 4 * c, v);
-    } else if (p.wide) {
-      MxFew<T, 2>::store(out + 2 * c, v);
-    } else {
-      out[2 * c] = from_f32<T>(v[0]);
-      if (2 * c + 1 < p.K) out[2 * c + 1] = from_f32<T>(v[1]);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int c = c0 + i * (int)blockDim.x;
+      if (W * c >= p.K) break;
+      const float s = FMT == kNvFp4 ? e4m3x2_to_f2(sb[i]).x : e8m0_to_f32(sb[i]);
+      float v[W];
+#pragma unroll
+      for (int e = 0; e < W / 2; ++e) {
+        const float2 f = FMT == kMxFp8 ? e4m3x2_to_f2(code[i][e]) : e2m1x2_to_f2(code[i][e]);
+        v[2 * e] = FMT == kNvFp4 ? f.x * s * rs : f.x * s;
+        v[2 * e + 1] = FMT == kNvFp4 ? f.y * s * rs : f.y * s;
+      }
+      if constexpr (W == 4) {
+        store_vec<T, 4>(out + 4 * c, v);
+      } else if (p.wide) {
+        MxFew<T, 2>::store(out + 2 * c, v);
+      } else {
+        out[2 * c] = from_f32<T>(v[0]);
+        if (2 * c + 1 < p.K) out[2 * c + 1] = from_f32<T>(v[1]);
+      }
     }
   }
 }
