@@ -646,6 +646,11 @@ struct MxFew {
   }
 };
 
+// Place of value e in shared memory: a chunk's four groups of four change places
+// with the chunk's number, so that neither the passes along the row nor the
+// chunks' 16-byte reads meet in a bank.
+__device__ __forceinline__ int mx_any_place(int e) { return e ^ (((e >> 5) & 3) << 2); }
+
 // E: values per access, two where all rows allow it.
 template <typename T, int FMT, bool kNorm, int E>
 __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowParams p) {
@@ -689,10 +694,10 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
           for (int k = 0; k < E; ++k) v[k] += w[k];
           MxFew<R, E>::store(ro + e, v);
         }
+        MxFew<float, E>::store(h + mx_any_place(e), v);
+        if constexpr (kNorm) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          h[e + k] = v[k];
-          if constexpr (kNorm) ss = fmaf(v[k], v[k], ss);
+          for (int k = 0; k < E; ++k) ss = fmaf(v[k], v[k], ss);
         }
       }
     }
@@ -701,7 +706,7 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
     pass(float{});
   else
     pass(T{});
-  for (int e = p.K + t; e < width; e += kMxAnyThreads) h[e] = 0.0f;
+  for (int e = p.K + t; e < width; e += kMxAnyThreads) h[mx_any_place(e)] = 0.0f;
   uint32_t top = 0;
   if constexpr (kNorm) {
     const float rstd = __frsqrt_rn(__fdiv_rn(row_sum<true>(ss, red_sum), (float)p.K) + p.eps);
@@ -717,14 +722,17 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
         for (int i = 0; i < B; ++i) {
           const int e = e0 + i * S;
           if (e >= p.K) break;
-          float f[E];
+          float f[E], y[E];
           w[i].get(f);
+          MxFew<float, E> held;
+          held.load(h + mx_any_place(e));
+          held.get(y);
 #pragma unroll
           for (int k = 0; k < E; ++k) {
-            const float y = __fmul_rn(__fmul_rn(h[e + k], rstd), f[k]);
-            h[e + k] = y;
-            if constexpr (FMT == kNvFp4) top = max(top, __float_as_uint(y) & 0x7FFFFFFFu);
+            y[k] = __fmul_rn(__fmul_rn(y[k], rstd), f[k]);
+            if constexpr (FMT == kNvFp4) top = max(top, __float_as_uint(y[k]) & 0x7FFFFFFFu);
           }
+          MxFew<float, E>::store(h + mx_any_place(e), y);
         }
       }
     };
@@ -735,7 +743,7 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
   } else if constexpr (FMT == kNvFp4) {
     for (int e0 = E * t; e0 < p.K; e0 += S)      // this thread's own
 #pragma unroll
-      for (int k = 0; k < E; ++k) top = max(top, __float_as_uint(h[e0 + k]) & 0x7FFFFFFFu);
+      for (int k = 0; k < E; ++k) top = max(top, __float_as_uint(h[mx_any_place(e0) + k]) & 0x7FFFFFFFu);
   }
   if constexpr (FMT == kNvFp4) top = row_max<true>(top, red_max);
   __syncthreads();
@@ -746,7 +754,7 @@ __global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowPa
     float v[kMxChunk];
 #pragma unroll
     for (int i = 0; i < kMxChunk; i += 4) {
-      const float4 f = c < chunks ? *reinterpret_cast<const float4*>(h + kMxChunk * c + i)
+      const float4 f = c < chunks ? *reinterpret_cast<const float4*>(h + mx_any_place(kMxChunk * c + i))
                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
     }
