@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(kCta ? 512 : 128) mx_row_kernel(const MxRowPar
 // stores are one segment, into shared memory as binary32; the chunks are taken
 // from there.  (Chunks of 16 straight from memory, element by element, touch a
 // sector per lane and load, and needed the row again for every step: 156 us for
-// the norm of 8704 x 4097 BF16.)  Now 82 us there, 3.1 TB/s, bound by its 2-byte
-// accesses, and 70 us at 8704 x 4098 in pairs.
+// the norm of 8704 x 4097 BF16.)  Now 76 us there, 3.3 TB/s, bound by its 2-byte
+// accesses, and 60 us at 8704 x 4098 in pairs.
 constexpr int kMxAnyThreads = 256;
 constexpr int kMxAnyCols = 49152;            // longest row held
 
@@ -651,9 +651,19 @@ struct MxFew {
 // chunks' 16-byte reads meet in a bank.
 __device__ __forceinline__ int mx_any_place(int e) { return e ^ (((e >> 5) & 3) << 2); }
 
+// CTAs per SM that the registers have to allow.  16-bit pairs with a norm: five
+// (four by themselves; 8704 x 4098 BF16 to mxfp8 67 -> 60 us; FP32 pairs would
+// spill, 1023 x 5102: 17 -> 21 us, and single values lose 6% for nvfp4).  Without
+// a norm: six (12288 x 4097 BF16 to mxfp4 56 -> 53 us; FP32 pairs 48 -> 51 us).
+template <typename T, bool kNorm, int E>
+constexpr int mx_any_ctas() {
+  if (E == 2 && sizeof(T) == 4) return 0;      // as the compiler likes
+  return kNorm ? (E == 2 ? 5 : 0) : 6;
+}
+
 // E: values per access, two where all rows allow it.
 template <typename T, int FMT, bool kNorm, int E>
-__global__ void __launch_bounds__(kMxAnyThreads) mx_row_any_kernel(const MxRowParams p) {
+__global__ void __launch_bounds__(kMxAnyThreads, mx_any_ctas<T, kNorm, E>()) mx_row_any_kernel(const MxRowParams p) {
   extern __shared__ __align__(16) float h[];   // the row's values, zeros past K
   __shared__ float red_sum[kMxAnyThreads / 32];
   __shared__ uint32_t red_max[kMxAnyThreads / 32];
