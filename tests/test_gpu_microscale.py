@@ -139,7 +139,7 @@ def test_dequantize_gives_nan_for_nan_blocks():
 
 # ------------------------------------------------------------------ norm
 
-def check_norm(x, weight, residual, fmt, eps, q, h):
+def check_norm(x, weight, residual, fmt, eps, q, h, d=2.0 ** -18):
     """y carries at most 64 binary32 roundings (the sum of squares: at most 40 in
     a thread and 14 across threads, halved by the root; division, eps, rsqrtf
     two units, two products, the sum h): |dy| <= 2^-18 |y|.  The codes have to
@@ -156,7 +156,6 @@ def check_norm(x, weight, residual, fmt, eps, q, h):
     else:
         assert h is None
     codes, bytes_, row = R.held(q)
-    d = 2.0 ** -18
     lo_scale, hi_scale = R.quantize(y * (1 - d), fmt), R.quantize(y * (1 + d), fmt)
     assert ((bytes_ >= np.minimum(lo_scale[1], hi_scale[1])) & (bytes_ <= np.maximum(lo_scale[1], hi_scale[1]))).all() \
         or fmt == "nvfp4"
@@ -343,6 +342,52 @@ def test_the_short_way_and_the_checked_one_agree():
     assert b.quantize(x[0], "mxfp8") is None and b.quantize(x.T, "mxfp8") is None and b.quantize(x, "mxfp6") is None
     assert b.matmul(q, q, None, 0) is None and b.matmul(y, y, bias[:3], 0) is None
     assert b.rotate(q, k[:, :, :3], rot, False) is None and b.rotate(q, k, rot._replace(axes=[64, 64]), False) is None
+
+
+# off the 16-byte boundaries: one value, two and four an access, lengths around a
+# CTA's steps, the longest row that is held on chip (49152 with its padding) and
+# the next
+OFF = [15, 18, 255, 258, 2047, 2050, 4097, 4098, 4100, 49118, 49151, 49153, 49154, 60001]
+
+
+@pytest.mark.parametrize("fmt", R.FORMATS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("K", OFF)
+def test_rows_off_the_boundaries(fmt, dt, K):
+    f = fqa()
+    x = rand(3, K, dt, K)
+    q = f.mx_quantize(x, fmt)
+    same_as_reference(q, x.double().cpu().numpy())
+    # the way back: exact in BF16 but for the row scales' binary32 product
+    v = f.mx_dequantize(q, 0).double().cpu().numpy()
+    want = R.values(*R.held(q), fmt, K)
+    assert (np.abs(v - want) <= (2.0 ** -8 + 2.0 ** -24) * np.abs(want)).all()
+    # and a view that starts inside a 16-byte piece holds what its copy holds
+    y = rand(3, K + 3, dt, K + 1)[:, 1:K + 1]
+    for a, b in zip(R.held(f.mx_quantize(y, fmt)), R.held(f.mx_quantize(y.clone(), fmt))):
+        assert (a is None and b is None) or np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", R.FORMATS)
+@pytest.mark.parametrize("dt,res,wt", [("bf16", "bf16", "bf16"), ("bf16", "f32", "f32"), ("f32", "f32", "f32"),
+                                       ("f16", None, "f32")])
+@pytest.mark.parametrize("K", OFF)
+def test_norm_off_the_boundaries(fmt, dt, res, wt, K):
+    f = fqa()
+    x = rand(3, K, dt, K, 1.0)
+    weight = (1 + 0.3 * torch.randn(K, device="cuda")).to(DT[wt])
+    residual = None if res is None else rand(3, K, res, K + 1, 1.0)
+    q, h = f.mx_rms_norm(x, weight, fmt, residual=residual, eps=1e-5)
+    # a thread adds up to 49152 / 256 = 192 squares in a row: (192 + 14) / 2 + 10
+    # roundings are 113 <= 2^7 of 2^-24
+    check_norm(x, weight, residual, fmt, 1e-5, q, h, 2.0 ** -17)
+    if res == dt:
+        for which in (0, 1):                     # residual_out = residual, and = x
+            xc, rc = x.clone(), residual.clone()
+            q2, h2 = f.mx_rms_norm(xc, weight, fmt, residual=rc, residual_out=(rc, xc)[which], eps=1e-5)
+            assert torch.equal(h, h2)
+            for a, b in zip(R.held(q), R.held(q2)):
+                assert (a is None and b is None) or np.array_equal(a, b)
 
 
 @pytest.mark.parametrize("K", [4096, 4097])
