@@ -285,8 +285,11 @@ static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, bool pairs, cud
   if (!vec && chunks * kMxChunk <= kMxAnyCols) {
     const int smem = chunks * kMxChunk * 4;
     const auto fn = pairs ? mx_row_any_kernel<T, FMT, kNorm, 2> : mx_row_any_kernel<T, FMT, kNorm, 1>;
-    if (smem > 48 * 1024 && cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 kMxAnyCols * 4) != cudaSuccess)
+    // the default limit of 48 KB holds the row and the kernel's own arrays (a row
+    // padded to 12288 values fills it alone)
+    if (smem + kMxAnyStatic > 48 * 1024 && cudaFuncSetAttribute((const void*)fn,
+                                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                                kMxAnyCols * 4) != cudaSuccess)
       return FQA_ERR_CUDA;
     return launch_overlapped(fn, p.M, kMxAnyThreads, smem, s, 1, p);
   }

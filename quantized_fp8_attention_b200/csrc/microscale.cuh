@@ -618,6 +618,8 @@ __global__ void __launch_bounds__(kCta ? 512 : 128) mx_row_kernel(const MxRowPar
 // accesses, and 60 us at 8704 x 4098 in pairs.
 constexpr int kMxAnyThreads = 256;
 constexpr int kMxAnyCols = 49152;            // longest row held
+constexpr int kMxAnyWarps = kMxAnyThreads / 32;
+constexpr int kMxAnyStatic = 2 * kMxAnyWarps * 4;   // shared memory beside the row: a word per warp for each reduction
 
 // E neighbours (E * sizeof(T) bytes aligned) as binary32, and back.
 template <typename T, int E>
@@ -665,8 +667,8 @@ constexpr int mx_any_ctas() {
 template <typename T, int FMT, bool kNorm, int E>
 __global__ void __launch_bounds__(kMxAnyThreads, mx_any_ctas<T, kNorm, E>()) mx_row_any_kernel(const MxRowParams p) {
   extern __shared__ __align__(16) float h[];   // the row's values, zeros past K
-  __shared__ float red_sum[kMxAnyThreads / 32];
-  __shared__ uint32_t red_max[kMxAnyThreads / 32];
+  __shared__ float red_sum[kMxAnyWarps];
+  __shared__ uint32_t red_max[kMxAnyWarps];
   grid_release();
   grid_wait();
   const int t = threadIdx.x, row = blockIdx.x;
