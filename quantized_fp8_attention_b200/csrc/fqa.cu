@@ -48,10 +48,21 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 std::once_flag g_encode_once;
 EncodeTiledFn g_encode = nullptr;
 
+// The answer to a failed runtime call, which keeps its error for whoever asks
+// next: taken here, so that a later launch's status is its own.
+static fqa_status cuda_failed() {
+  cudaGetLastError();
+  return FQA_ERR_CUDA;
+}
+
+static fqa_status launch_status() {
+  return cudaGetLastError() == cudaSuccess ? FQA_OK : FQA_ERR_CUDA;
+}
+
 static uint32_t* status_ptr(fqa_status* st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    *st = FQA_ERR_CUDA;
+    *st = cuda_failed();
     return nullptr;
   }
   DeviceCache& c = g_dev[dev];
@@ -62,7 +73,7 @@ static uint32_t* status_ptr(fqa_status* st) {
     if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         p == nullptr || sms <= 0) {
-      *st = FQA_ERR_CUDA;
+      *st = cuda_failed();
       return nullptr;
     }
     c.num_sms = sms;
@@ -181,9 +192,6 @@ static fqa_status check_shape(int B, int H, int N, int d) {
   return FQA_OK;
 }
 
-static fqa_status launch_status() {
-  return cudaGetLastError() == cudaSuccess ? FQA_OK : FQA_ERR_CUDA;
-}
 
 // SM count of the current device (valid once status_ptr() succeeded on it).
 static int num_sms() {
@@ -200,13 +208,13 @@ static fqa_status launch_attention_bf16(const void* q, const void* k, const void
   CUtensorMap tq, tk, tv;
   if (!make_tmap(&tq, q, false, prm.N, heads) || !make_tmap(&tk, k, false, prm.N, heads) ||
       !make_tmap(&tv, v, false, prm.N, heads))
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   if (cudaFuncSetAttribute(attn_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            BfTraits::kSmemBytes) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   const int items = prm.B * prm.H * ((prm.N + kPairRows - 1) / kPairRows);
   const int sms = num_sms();
-  if (sms <= 0) return FQA_ERR_CUDA;
+  if (sms <= 0) return cuda_failed();
   const int grid = items < sms ? items : sms;
   attn_bf16_kernel<<<grid, kWsThreads, BfTraits::kSmemBytes, stream>>>(tq, tk, tv, prm);
   return launch_status();
@@ -220,7 +228,7 @@ static fqa_status launch_attention_fp8(const void* q, const void* k, const void*
   CUtensorMap tq, tk, tv;
   if (!make_tmap(&tq, q, true, prm.N, heads) || !make_tmap(&tk, k, true, prm.N, heads) ||
       !make_tmap(&tv, v, true, prm.N, heads))
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   // the instance that carries only what the call needs: the short-tail patch
   // when N is not a multiple of 128, the key mask and row statistics when
   // given
@@ -234,10 +242,10 @@ static fqa_status launch_attention_fp8(const void* q, const void* k, const void*
   if (prm.patch && !tail && prm.kmask != nullptr) fn = attn_fp8_kernel<false, false, true>;
   if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            F8Traits::kSmemBytes) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   const int items = prm.B * prm.H * ((prm.N + 2 * kBlockM - 1) / (2 * kBlockM));
   const int sms = num_sms();
-  if (sms <= 0) return FQA_ERR_CUDA;
+  if (sms <= 0) return cuda_failed();
   const int grid = items < sms ? items : sms;
   fn<<<grid, kF8Threads, F8Traits::kSmemBytes, stream>>>(tq, tk, tv, prm);
   return launch_status();
@@ -266,8 +274,7 @@ static fqa_status launch_overlapped(void (*fn)(P...), dim3 grid, dim3 block, int
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...) != cudaSuccess) return FQA_ERR_CUDA;
-  return launch_status();
+  return cudaLaunchKernelEx(&cfg, fn, std::forward<A>(args)...) == cudaSuccess ? FQA_OK : cuda_failed();
 }
 
 // One launch of the row kernel that fits the row: 16 elements a thread and
@@ -290,7 +297,7 @@ static fqa_status launch_mx_rows(const MxRowParams& p, bool vec, bool pairs, cud
     if (smem + kMxAnyStatic > 48 * 1024 && cudaFuncSetAttribute((const void*)fn,
                                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                                 kMxAnyCols * 4) != cudaSuccess)
-      return FQA_ERR_CUDA;
+      return cuda_failed();
     return launch_overlapped(fn, p.M, kMxAnyThreads, smem, s, 1, p);
   }
   if (!vec) return launch_overlapped(mx_row_kernel<T, FMT, kNorm, true, 1, true, false>, p.M, 512, 0, s, 1, p);
@@ -344,7 +351,7 @@ static fqa_status launch_mx_small(const uint8_t* a, const uint8_t* b, const MxMa
                                   cudaStream_t s) {
   using T = MxSmall<FMT, NT>;
   CUtensorMap tp, tq;
-  if (!make_tmap_rows(&tp, b, row_bytes, p.N, 128) || !make_tmap_rows(&tq, a, row_bytes, p.M, NT)) return FQA_ERR_CUDA;
+  if (!make_tmap_rows(&tp, b, row_bytes, p.N, 128) || !make_tmap_rows(&tq, a, row_bytes, p.M, NT)) return cuda_failed();
   const int64_t tiles = (int64_t)((p.N + 127) / 128) * ((p.M + NT - 1) / NT);
   // split K while all CTAs are resident at once and each keeps two stages; a
   // cluster of eight wants that many free SMs in one GPC, so only up to three
@@ -357,7 +364,7 @@ static fqa_status launch_mx_small(const uint8_t* a, const uint8_t* b, const MxMa
   if (tiles * ranks > INT32_MAX) return FQA_ERR_UNSUPPORTED;
   const auto fn = mx_matmul_small_kernel<FMT, NT>;
   if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   return launch_overlapped(fn, dim3((unsigned)(tiles * ranks)), kMxSmallThreads, T::kSmemBytes, s, ranks, tp, tq, p,
                            ranks);
 }
@@ -375,10 +382,10 @@ static fqa_status launch_mx_large(const uint8_t* a, const uint8_t* b, const MxMa
       !make_tmap_scales(&tsa, p.sa, p.KT, p.M, MxMma<FMT>::kWords, 1) ||
       !make_tmap_scales(&tsb, p.sb, p.KT, p.N, MxMma<FMT>::kWords, 2) ||
       (tma_out && !make_tmap_out(&to, p.out, p.out_type, p.M, p.N)))
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   const auto fn = mx_matmul_large_kernel<FMT>;
   if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   return launch_overlapped(fn, dim3(2 * (unsigned)std::min<int64_t>(tiles, num_sms() / 2)), kMxLargeThreads,
                            T::kSmemBytes, s, 2, ta, tb, tsa, tsb, to, p, (int)tma_out);
 }
@@ -466,16 +473,16 @@ static fqa_status quantize_impl(const void* q, const void* k, const void* v, int
   const int nunits = B * H * ((N + kQBlock - 1) / kQBlock);
   if (cudaFuncSetAttribute(quantize_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kQuantSmem) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, quantize_fused_kernel, kQuantThreads,
                                                     kQuantSmem) != cudaSuccess ||
       per_sm < 1)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   int grid = per_sm * num_sms();
   if (grid > nunits) grid = nunits;
   static_assert(kNumCtr * sizeof(unsigned int) <= 256, "counters fit the reserved 256 bytes");
-  if (cudaMemsetAsync(ctr, 0, kNumCtr * sizeof(unsigned int), s) != cudaSuccess) return FQA_ERR_CUDA;
+  if (cudaMemsetAsync(ctr, 0, kNumCtr * sizeof(unsigned int), s) != cudaSuccess) return cuda_failed();
   const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(q);
   const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(k);
   const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(v);
@@ -490,7 +497,7 @@ static fqa_status quantize_impl(const void* q, const void* k, const void* v, int
   // a CTA that never starts
   if (cudaLaunchCooperativeKernel((const void*)quantize_fused_kernel, dim3(grid), dim3(kQuantThreads),
                                   args, kQuantSmem, s) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   return launch_status();
 }
 
@@ -637,7 +644,7 @@ fqa_status fqa_select_keys(const float* k_err, int B, int H, int N, int kc, uint
   const int smem = staged ? N * 4 : 0;
   if (staged && cudaFuncSetAttribute(select_keys_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kSelStageMax * 4) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   select_keys_kernel<<<B * H, kSelThreads, smem, static_cast<cudaStream_t>(cuda_stream)>>>(k_err, N, kc, kmask,
                                                                                          idx, staged);
   return launch_status();
@@ -703,10 +710,10 @@ fqa_status fqa_attention_fp8_corrected(const void* q, const void* k, const void*
   if (prm.patch) {
     // take the copied keys' terms out of the patched FP8 part's row sums
     CUtensorMap tq8;
-    if (!make_tmap(&tq8, q8, true, N, B * H)) return FQA_ERR_CUDA;
+    if (!make_tmap(&tq8, q8, true, N, B * H)) return cuda_failed();
     if (cudaFuncSetAttribute(dup_sum_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDupSmem) !=
         cudaSuccess)
-      return FQA_ERR_CUDA;
+      return cuda_failed();
     DupParams dp{static_cast<const uint8_t*>(k8), sq, sk, kmask, stats, N, softmax_scale, status};
     dup_sum_kernel<<<dim3(N / kBlockM, B * H), kDupThreads, kDupSmem, s>>>(tq8, dp);
     if ((st = launch_status()) != FQA_OK) return st;
@@ -714,7 +721,7 @@ fqa_status fqa_attention_fp8_corrected(const void* q, const void* k, const void*
   // exact part over the corrected keys, merged into the output: one chunk of
   // 64 (two CTAs per SM; three of its rows carry the K mean) when they fit
   CUtensorMap tq;
-  if (!make_tmap(&tq, q, false, N, B * H)) return FQA_ERR_CUDA;
+  if (!make_tmap(&tq, q, false, N, B * H)) return cuda_failed();
   CorrParams cp{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
                 static_cast<const __nv_bfloat16*>(v), k_mean, idx, o1, stats, prm.patch, out,
                 out_dtype == FQA_OUT_F32, B, H, N, kc, softmax_scale, status};
@@ -722,7 +729,7 @@ fqa_status fqa_attention_fp8_corrected(const void* q, const void* k, const void*
   const void* fn = small ? (const void*)correct_kernel<64> : (const void*)correct_kernel<128>;
   const int smem = small ? CorrTraits<64>::kSmemBytes : CorrTraits<128>::kSmemBytes;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   const int sms = num_sms() * (small ? CorrTraits<64>::kCtasPerSm : CorrTraits<128>::kCtasPerSm);
   const int ntq = (N + 127) / 128;
   int split = (sms + B * H - 1) / (B * H);       // about one wave of CTAs
@@ -778,18 +785,18 @@ fqa_status fqa_attention_nvfp4(const uint8_t* q4, const uint8_t* k4, const uint8
   CUtensorMap tq, tk, tv;
   if (!make_tmap_fp4(&tq, q4, N, heads) || !make_tmap_fp4(&tk, k4, N, heads) ||
       !make_tmap(&tv, v8, true, N, heads))
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   // the short-tail instance only when N is not a multiple of 128
   const bool tail = N % kBlockN != 0;
   using NvKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const NvParams);
   const NvKernel fn = tail ? attn_nvfp4_kernel<true> : attn_nvfp4_kernel<false>;
   if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, NvTraits::kSmemBytes) !=
       cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   NvParams prm{B, H, N, softmax_scale, sfq, sfk, sq1, sk1, sv, sv_max, out, out_dtype == FQA_OUT_F32, status};
   const int items = heads * ((N + kBlockM - 1) / kBlockM);
   const int sms = num_sms();
-  if (sms <= 0) return FQA_ERR_CUDA;
+  if (sms <= 0) return cuda_failed();
   const int grid = items < sms ? items : sms;
   fn<<<grid, kNvThreads, NvTraits::kSmemBytes, static_cast<cudaStream_t>(cuda_stream)>>>(tq, tk, tv, prm);
   return launch_status();
@@ -1035,7 +1042,7 @@ fqa_status fqa_exp2_error(float lo, float hi, uint32_t* max_rel_bits, void* cuda
   std::memcpy(&lb, &lo, 4);
   const uint32_t n = lb - hb + 1;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  if (cudaMemsetAsync(max_rel_bits, 0, 4, s) != cudaSuccess) return FQA_ERR_CUDA;
+  if (cudaMemsetAsync(max_rel_bits, 0, 4, s) != cudaSuccess) return cuda_failed();
   exp2_error_kernel<<<148 * 16, 256, 0, s>>>(lb, n, reinterpret_cast<unsigned int*>(max_rel_bits));
   return launch_status();
 }
@@ -1060,10 +1067,10 @@ fqa_status fqa_debug_wait_timeout(uint32_t limit_us, void* cuda_stream) {
 
 fqa_status fqa_debug_status(void* cuda_stream, uint32_t* flags_out) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess)
-    return FQA_ERR_CUDA;
+    return cuda_failed();
   uint32_t v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_word, sizeof(v)) != cudaSuccess) return FQA_ERR_CUDA;
-  if (cudaMemcpyToSymbol(g_status_word, &zero, sizeof(zero)) != cudaSuccess) return FQA_ERR_CUDA;
+  if (cudaMemcpyFromSymbol(&v, g_status_word, sizeof(v)) != cudaSuccess) return cuda_failed();
+  if (cudaMemcpyToSymbol(g_status_word, &zero, sizeof(zero)) != cudaSuccess) return cuda_failed();
   if (flags_out) *flags_out = v;
   return (v & kStatusTimeout) ? FQA_ERR_TIMEOUT : FQA_OK;
 }
@@ -1099,7 +1106,7 @@ NoAllocCache g_noalloc[kMaxDevices];
 static float* noalloc_scratch(fqa_status* st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    *st = FQA_ERR_CUDA;
+    *st = cuda_failed();
     return nullptr;
   }
   NoAllocCache& c = g_noalloc[dev];
@@ -1107,7 +1114,7 @@ static float* noalloc_scratch(fqa_status* st) {
   if (c.ptr == nullptr) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || p == nullptr) {
-      *st = FQA_ERR_CUDA;
+      *st = cuda_failed();
       return nullptr;
     }
     c.ptr = static_cast<float*>(p);
