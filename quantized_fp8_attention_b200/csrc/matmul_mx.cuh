@@ -650,11 +650,11 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
       if (cols) {
         bar_sync(1, 256);            // everyone is through with the last tile's
         const int n = ni * 256 + et;
-        sc[et] = (p.rb != nullptr && n < p.N) ? __ldg(p.rb + n) : 1.0f;
-        sc[256 + et] = (p.bias != nullptr && n < p.N) ? __ldg(p.bias + n) : 0.0f;
+        sc[et] = (p.rb != nullptr && n < p.N) ? p.rb[n] : 1.0f;
+        sc[256 + et] = (p.bias != nullptr && n < p.N) ? p.bias[n] : 0.0f;
         bar_sync(1, 256);
       }
-      const float ra = (p.ra != nullptr && row0 + lane < p.M) ? __ldg(p.ra + row0 + lane) : 1.0f;
+      const float ra = (p.ra != nullptr && row0 + lane < p.M) ? p.ra[row0 + lane] : 1.0f;
       ok = ok && warp_wait(acc_full, done & 1, abort_flag, p.status);
       if (!ok) continue;
       tc_fence_after();

@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const MxDequantParam
   if (row >= p.M) return;
   const uint8_t* sf = p.scales + (size_t)(row >> 7) * p.KT * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
   const uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
-  const float rs = FMT == kNvFp4 ? __ldg(p.row_scale + row) : 1.0f;
+  const float rs = FMT == kNvFp4 ? p.row_scale[row] : 1.0f;
   T* out = static_cast<T*>(p.out) + (int64_t)row * p.K;
   for (int c = threadIdx.x; kMxChunk * c < p.K; c += blockDim.x) {
     const int blk = kMxChunk * c / kBlock;
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantP
   if (row >= p.M) return;
   const uint8_t* sf = p.scales + (size_t)(row >> 7) * p.KT * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
   const uint8_t* codes = p.codes + (size_t)row * (p.Kp / mx_per_byte(FMT));
-  const float rs = FMT == kNvFp4 ? __ldg(p.row_scale + row) : 1.0f;
+  const float rs = FMT == kNvFp4 ? p.row_scale[row] : 1.0f;
   T* out = static_cast<T*>(p.out) + (int64_t)row * p.K;
   constexpr int B = 4;                           // groups a thread has in flight
   for (int c0 = threadIdx.x; W * c0 < p.K; c0 += B * blockDim.x) {
