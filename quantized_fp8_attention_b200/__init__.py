@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -27,7 +28,7 @@ FQA_OUT_F16 = 2            # mx_matmul and mx_dequantize only
 HEAD_DIM = 128
 
 _lib = None
-_native = None             # csrc/binding.cpp: the everyday calls without the interpreter
+_native = None             # csrc/binding.cpp: the everyday calls without the interpreter (or _CheckedWay)
 
 
 def _load():
@@ -95,19 +96,39 @@ def _load():
     L.fqa_rotary.restype = I
     L.fqa_rotary.argtypes = [P, P, I, I, I, I, I, I, Q, Q, Q, Q, Q, Q, P, I, Q, I, P, ctypes.c_double, I, P, P,
                              ctypes.c_float, P, P, P]
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise ImportError(f"_binding.so is not built or does not load ({e}); run "
-                          "`python -m quantized_fp8_attention_b200.build`.") from None
-    _binding.init(LIB_PATH, Microscaled, Rotary)
     global _native
-    _native = _binding
+    _native = _short_way()
     _lib = L
     return L
 
 
+class _CheckedWay:
+    """Stands in for csrc/binding.cpp where that is not built for this torch and
+    Python: answers None, so every call takes the functions below, 10 to 15 us
+    slower on the host."""
+
+    @staticmethod
+    def quantize(*args):
+        return None
+
+    dequantize = rms_norm = matmul = rotate = quantize
+
+
 def _short_way():
+    from . import build
+    try:
+        if not build.binding_fits():
+            raise ImportError("it is absent or built for another torch or Python")
+        from . import _binding
+        _binding.init(LIB_PATH, Microscaled, Rotary)
+        return _binding
+    except ImportError as e:
+        warnings.warn(f"_binding.so does not serve ({e}): calls take the slower way through Python; run "
+                      "`python -m quantized_fp8_attention_b200.build`.", RuntimeWarning, stacklevel=4)
+        return _CheckedWay
+
+
+def _native_calls():
     _load()
     return _native
 
@@ -731,7 +752,7 @@ def mx_quantize(x: torch.Tensor, fmt: str, out: Optional[Microscaled] = None, st
     """Rows [..., K] of bfloat16, float16 or float32 -> Microscaled rows (leading
     dimensions flattened).  A block (nvfp4: a row) with a NaN or an infinity
     stands for NaN."""
-    if out is None and stream is None and (q := (_native or _short_way()).quantize(x, fmt)) is not None:
+    if out is None and stream is None and (q := (_native or _native_calls()).quantize(x, fmt)) is not None:
         return q
     index = _device_tensor(x, "x")
     if (there := _elsewhere(index, stream, (x, *(() if out is None else out[:3])))) is not None:
@@ -751,7 +772,7 @@ def mx_quantize(x: torch.Tensor, fmt: str, out: Optional[Microscaled] = None, st
 def mx_dequantize(q: Microscaled, out_dtype: int = FQA_OUT_BF16, out: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """The values that microscaled rows stand for, [M, cols]."""
-    if out is None and stream is None and (v := (_native or _short_way()).dequantize(q, out_dtype)) is not None:
+    if out is None and stream is None and (v := (_native or _native_calls()).dequantize(q, out_dtype)) is not None:
         return v
     M, code, index = _require_microscaled(q, "q")
     if (there := _elsewhere(index, stream, (*q[:3], out))) is not None:
@@ -779,7 +800,7 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, fmt: str = "mxfp8", resid
     residual).  weight [K] and residual are of x's type or float32.
     residual_out may be residual itself (or x, where of the same type)."""
     if out is None and residual_out is None and stream is None and (
-            y := (_native or _short_way()).rms_norm(x, weight, fmt, residual, eps)) is not None:
+            y := (_native or _native_calls()).rms_norm(x, weight, fmt, residual, eps)) is not None:
         return y
     index = _device_tensor(x, "x")
     if (there := _elsewhere(index, stream, (x, weight, residual, residual_out, *(() if out is None else out[:3])))) is not None:
@@ -824,7 +845,7 @@ def mx_matmul(a: Microscaled, b: Microscaled, bias: Optional[torch.Tensor] = Non
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """a [M, K] times the transpose of b [N, K] (a projection's weights), both
     microscaled rows of one format, plus a float32 bias [N]: [M, N]."""
-    if out is None and stream is None and (y := (_native or _short_way()).matmul(a, b, bias, out_dtype)) is not None:
+    if out is None and stream is None and (y := (_native or _native_calls()).matmul(a, b, bias, out_dtype)) is not None:
         return y
     M, code, index = _require_microscaled(a, "a")
     N, other, _ = _require_microscaled(b, "b", index)
@@ -885,7 +906,7 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], rot: Rotary, inverse: boo
     weights) and rotated, contiguous.  `inverse` rotates back.  An output may be
     its own input where that is contiguous."""
     if q_out is None and k_out is None and stream is None and (
-            y := (_native or _short_way()).rotate(q, k, rot, inverse)) is not None:
+            y := (_native or _native_calls()).rotate(q, k, rot, inverse)) is not None:
         return y
     index = _device_tensor(q, "q")
     if not isinstance(rot, Rotary):
