@@ -523,6 +523,22 @@ FQA_API fqa_status fqa_e4m3_encode(const float* x, uint8_t* out, size_t n, void*
 FQA_API fqa_status fqa_debug_wait_timeout(uint32_t limit_us, void* cuda_stream);
 
 /*
+ * fqa_debug_mx_matmul_timeout -- checks the bounded waits of fqa_mx_matmul():
+ * the same call with its waits limited to 1.5 milliseconds, in which CTA `rank`
+ * (0 .. 7; -1: every CTA) of each cluster that works on a tile loads nothing
+ * from its stage `stage` (0 .. 2^24) on.  What waits for that stage gives up;
+ * the kernel waits for its own copies and products in flight and returns,
+ * leaving the context usable.  The next fqa_debug_status() then returns
+ * FQA_ERR_TIMEOUT, and `out` holds anything (FQA_OK where the call has no such
+ * stage: its result is then that of fqa_mx_matmul()).
+ */
+FQA_API fqa_status fqa_debug_mx_matmul_timeout(const uint8_t* a_codes, const uint8_t* a_scales,
+                                               const float* a_row_scale, const uint8_t* b_codes,
+                                               const uint8_t* b_scales, const float* b_row_scale, const float* bias,
+                                               int M, int N, int K, fqa_mx_format fmt, void* out,
+                                               fqa_dtype out_dtype, int rank, int stage, void* cuda_stream);
+
+/*
  * fqa_debug_status -- synchronizes cuda_stream, reads and clears the
  * device status word of the current device.  Returns FQA_ERR_TIMEOUT if a
  * bounded device wait gave up since the last call, FQA_ERR_CUDA if the

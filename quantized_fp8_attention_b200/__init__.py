@@ -300,6 +300,21 @@ def fqa_debug_wait_timeout(limit_us: int, stream=None) -> int:
     return L.fqa_debug_wait_timeout(int(limit_us), _stream(stream))
 
 
+def fqa_debug_mx_matmul_timeout(a: "Microscaled", b: "Microscaled", out: torch.Tensor, out_dtype: int, rank: int = -1,
+                                stage: int = 0, stream=None) -> int:
+    """mx_matmul(a, b) into out with loads that stop at a stage and waits that
+    give up early (the next fqa_debug_status() reports FQA_ERR_TIMEOUT)."""
+    L = _load()
+    P, I = ctypes.c_void_p, ctypes.c_int
+    L.fqa_debug_mx_matmul_timeout.restype = I
+    L.fqa_debug_mx_matmul_timeout.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, I, I, I, P]
+    M, code, _ = _require_microscaled(a, "a")
+    N = _require_microscaled(b, "b")[0]
+    return L.fqa_debug_mx_matmul_timeout(_ptr(a.codes), _ptr(a.scales), _ptr(a.row_scale), _ptr(b.codes), _ptr(b.scales),
+                                         _ptr(b.row_scale), None, M, N, a.cols, code, _ptr(out), int(out_dtype),
+                                         int(rank), int(stage), _stream(stream))
+
+
 def fqa_debug_status(stream=None):
     """(status, raw flag bits) of the current device's status word; clears it."""
     flags = ctypes.c_uint32(0)

@@ -910,10 +910,11 @@ fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales, const 
   return launch_mx_dequantize_format<float>(p, fmt, vec >= 16, s);
 }
 
-fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,
-                         const uint8_t* b_codes, const uint8_t* b_scales, const float* b_row_scale,
-                         const float* bias, int M, int N, int K, fqa_mx_format fmt, void* out, fqa_dtype out_dtype,
-                         void* cuda_stream) {
+// fqa_mx_matmul(), and its check (stop: see loads_until()).
+static fqa_status mx_matmul_checked(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,
+                                    const uint8_t* b_codes, const uint8_t* b_scales, const float* b_row_scale,
+                                    const float* bias, int M, int N, int K, int fmt, void* out, int out_dtype,
+                                    void* cuda_stream, uint32_t stop) {
   if (!mx_format_ok(fmt) || !dtype_ok(out_dtype) || M < 0 || N < 0 || K < 1) return FQA_ERR_INVALID_ARG;
   if (!mx_shape_ok(M, K) || !mx_shape_ok(N, K)) return FQA_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return FQA_OK;
@@ -934,11 +935,19 @@ fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const 
   const int row_bytes = mx_padded(K) / mx_per_byte(fmt);
   const bool nv = fmt == FQA_NVFP4;
   const MxMatmulParams p{a_scales, b_scales, nv ? a_row_scale : nullptr, nv ? b_row_scale : nullptr, bias, out, M, N,
-                         (row_bytes + 31) / 32, mx_words(K, fmt), (int)out_dtype, status};
+                         (row_bytes + 31) / 32, mx_words(K, fmt), out_dtype, stop, status};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (fmt == FQA_MXFP8) return launch_mx_matmul<kMxFp8>(a_codes, b_codes, p, row_bytes, s);
   if (fmt == FQA_MXFP4) return launch_mx_matmul<kMxFp4>(a_codes, b_codes, p, row_bytes, s);
   return launch_mx_matmul<kNvFp4>(a_codes, b_codes, p, row_bytes, s);
+}
+
+fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,
+                         const uint8_t* b_codes, const uint8_t* b_scales, const float* b_row_scale,
+                         const float* bias, int M, int N, int K, fqa_mx_format fmt, void* out, fqa_dtype out_dtype,
+                         void* cuda_stream) {
+  return mx_matmul_checked(a_codes, a_scales, a_row_scale, b_codes, b_scales, b_row_scale, bias, M, N, K, fmt, out,
+                           out_dtype, cuda_stream, kMxNoStop);
 }
 
 // ------------------------------------------------------------- rotary
@@ -1063,6 +1072,15 @@ fqa_status fqa_debug_wait_timeout(uint32_t limit_us, void* cuda_stream) {
   wait_timeout_kernel<<<1, 1, 0, static_cast<cudaStream_t>(cuda_stream)>>>(
       status, (uint64_t)limit_us * 1000ull);
   return launch_status();
+}
+
+fqa_status fqa_debug_mx_matmul_timeout(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,
+                                       const uint8_t* b_codes, const uint8_t* b_scales, const float* b_row_scale,
+                                       const float* bias, int M, int N, int K, fqa_mx_format fmt, void* out,
+                                       fqa_dtype out_dtype, int rank, int stage, void* cuda_stream) {
+  if (rank < -1 || rank > 7 || stage < 0 || stage > 1 << 24) return FQA_ERR_INVALID_ARG;
+  return mx_matmul_checked(a_codes, a_scales, a_row_scale, b_codes, b_scales, b_row_scale, bias, M, N, K, fmt, out,
+                           out_dtype, cuda_stream, 16u * (uint32_t)stage + (uint32_t)(rank + 1));
 }
 
 fqa_status fqa_debug_status(void* cuda_stream, uint32_t* flags_out) {

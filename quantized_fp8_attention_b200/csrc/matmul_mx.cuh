@@ -18,6 +18,7 @@
 // results, so the scale tiles' rows past the end need no value.
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "attention.cuh"
@@ -108,9 +109,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-// mbar_wait() by a whole warp: one answer for all lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
+// mbar_wait_limit() by a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_limit(bar, parity, abort_flag, status, limit_ns));
 }
 
 // Shared address of the same offset in CTA `rank` of the cluster.
@@ -154,8 +156,24 @@ struct MxMatmulParams {
   int mmas;               // MMAs of a row: 32-byte steps over its codes
   int KT;                 // scale words of a row
   int out_type;           // 0 BF16, 1 binary32, 2 FP16
+  uint32_t stop;          // kMxNoStop, or a check of the waits: 16 * stage + rank + 1
   uint32_t* status;
 };
+// (one word for the check, where the struct had padding: 16 more bytes of
+// parameters cost each launch 0.35 us on the host)
+constexpr uint32_t kMxNoStop = 0xFFFFFFFFu;
+static_assert(sizeof(MxMatmulParams) == 80, "no larger");
+
+// In a check of the waits (fqa_debug_mx_matmul_timeout()) CTA `rank` of a cluster
+// (-1: each) loads nothing from its stage `stage` on, so that what waits for it
+// runs into its limit, a short one.
+__device__ __forceinline__ int loads_until(const MxMatmulParams& p, int rank) {
+  const uint32_t who = p.stop & 15u;
+  return who == 0 || who == (uint32_t)rank + 1 ? (int)(p.stop >> 4) : INT_MAX;
+}
+__device__ __forceinline__ uint64_t wait_limit(const MxMatmulParams& p) {
+  return p.stop == kMxNoStop ? kWaitLimitNs : kWaitLimitNs / 1000;
+}
 
 // ------------------------------------------------------- few rows of A
 //
@@ -219,6 +237,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   const int stages = (p.mmas + 3) / 4;
   // this rank's stages: [s0, s1), an even share
   const int s0 = (int)((int64_t)stages * rank / ranks), s1 = (int)((int64_t)stages * (rank + 1) / ranks);
+  const int loads = min(s1 - s0, loads_until(p, rank));   // stages it loads
 
   auto load_stage = [&](int s, int slot) {         // one thread
     uint8_t* st = smem + slot * T::kStageBytes;
@@ -241,7 +260,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     mbar_fence_init();
     grid_wait();
     // the ring's first fill needs nothing else of the CTA
-    for (int s = s0; s < min(s1, s0 + T::kStages); ++s) load_stage(s, s - s0);
+    for (int i = 0; i < min(loads, T::kStages); ++i) load_stage(s0 + i, i);
   }
   __syncwarp();
   if (warp == 1) {
@@ -258,19 +277,16 @@ __global__ void __launch_bounds__(kMxSmallThreads)
 
   // (both issuing warps stay whole and elect a lane per step: see the issuer of
   // the large kernel)
+  int issued = 0;                    // warp 0: stages loaded
   if (warp == 0) {
-    int issued = min(s1 - s0, T::kStages);
-    for (int s = s0 + issued; s < s1; ++s) {
-      const int i = s - s0, slot = i % T::kStages;
-      if (!warp_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status)) break;
-      if (elect_one()) load_stage(s, slot);
+    issued = min(loads, T::kStages);
+    for (int i = issued; i < loads; ++i) {
+      const int slot = i % T::kStages;
+      if (!warp_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status, wait_limit(p))) break;
+      if (elect_one()) load_stage(s0 + i, slot);
       __syncwarp();
       issued = i + 1;
     }
-    if (*abort_flag)        // no copy may be in flight when the CTA ends
-      for (int i = issued > T::kStages ? issued - T::kStages : 0; i < issued; ++i)
-        mbar_wait_drain(&full[i % T::kStages], (i / T::kStages) & 1);
-    __syncwarp();
   } else if (warp == 1) {
     constexpr uint32_t kI = Mma::idesc(128, NT);
     // the Q tile's place in its block of 128 rows: 32 rows per column (a tile of
@@ -278,7 +294,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     const uint32_t qcol = (uint32_t)(q0 % 128) / 32;
     for (int s = s0; s < s1; ++s) {
       const int i = s - s0, slot = i % T::kStages;
-      if (!warp_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status)) break;
+      if (!warp_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status, wait_limit(p))) break;
       tc_fence_after();
       const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
       const uint32_t sf = st + T::kStageBytes - 2 * T::kSfBytes;
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   };
   bool ok = true;
   if (warp >= 2) {
-    ok = warp_wait(done, 0, abort_flag, p.status);
+    ok = warp_wait(done, 0, abort_flag, p.status, wait_limit(p));
     tc_fence_after();
   }
   if (ranks > 1) cluster_wait();
@@ -398,6 +414,11 @@ __global__ void __launch_bounds__(kMxSmallThreads)
       }
   }
   __syncthreads();
+  // after a wait that gave up, in whichever warp: no copy may be in flight when
+  // the CTA ends
+  if (warp == 0 && *abort_flag)
+    for (int i = max(0, issued - T::kStages); i < issued; ++i)
+      mbar_wait_drain(&full[i % T::kStages], (i / T::kStages) & 1);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, T::kCols);
@@ -430,6 +451,10 @@ __global__ void __launch_bounds__(kMxSmallThreads)
 // formats, the operands' way from L2 (without loads the second takes 144 us).
 constexpr int kMxLargeThreads = 384;
 
+// Words by which a pair parts (part_after_giving_up()): kept by each CTA for
+// itself, then what both know.
+enum : int { kLoaded, kStagesOut, kTilesOut, kGaveUp, kLoaded0, kLoaded1, kStagesBoth, kTilesBoth, kNotes };
+
 template <int FMT>
 struct MxLarge {
   using Mma = MxMma<FMT>;
@@ -442,7 +467,8 @@ struct MxLarge {
   static constexpr int kOffOut = kStages * kStageBytes;      // 8 warps x 4 KB
   static constexpr int kOffCol = kOffOut + 8 * 4096;         // row scales and bias of the tile's columns
   static constexpr int kOffBar = kOffCol + 2 * 256 * 4;
-  static constexpr int kSmemBytes = kOffBar + (2 * kStages + 2) * 8 + 16 + 1024;
+  static constexpr int kOffNote = kOffBar + (2 * kStages + 2) * 8 + 16;   // kNotes words
+  static constexpr int kSmemBytes = kOffNote + kNotes * 4 + 1024;
   static constexpr int kColSf = 256, kSfCols = 12 * Mma::kWords;
   static_assert(kColSf + kStages * kSfCols <= 512, "tensor memory");
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -491,6 +517,59 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// A note in both CTAs of the pair.
+__device__ __forceinline__ void note_pair(int* note, int v) {
+  for (uint32_t r = 0; r < 2; ++r)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_u32(smem_u32(note), r)), "r"(v) : "memory");
+}
+// Takes bytes off what the barrier's phase still expects.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// The pair's end after a wait that gave up, in either CTA.  Nothing may reach a CTA
+// after it ends, nor an MMA run on, so both wait here (again with a limit) for
+//  - the commits that were issued: each stage's MMAs end with one to both CTAs, so
+//    these are the MMAs too.  The last on each barrier is enough: the one before
+//    was seen here before the issuer could get as far;
+//  - the copies in flight, whose bytes complete on the leader's barriers.  A stage
+//    that only one CTA loaded would never complete: the leader takes the other's
+//    bytes off what it expected, or makes the arrival that it owes with the
+//    other's bytes alone.
+// (Not inlined: what follows it in the kernel stays next to what comes before.)
+template <typename T>
+__device__ __noinline__ void part_after_giving_up(volatile int* note, uint32_t rank, uint64_t* full, uint64_t* empty,
+                                                  uint64_t* acc_full) {
+  constexpr int S = T::kStages;
+  if (threadIdx.x == 0) {
+    note_pair((int*)note + kLoaded0 + rank, note[kLoaded]);
+    if (rank == 0) {
+      note_pair((int*)note + kStagesBoth, note[kStagesOut]);
+      note_pair((int*)note + kTilesBoth, note[kTilesOut]);
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  if (threadIdx.x == 0) {
+    const int n0 = note[kLoaded0], n1 = note[kLoaded1], n = max(n0, n1);
+    const int stages = note[kStagesBoth], tiles = note[kTilesBoth];
+    for (int j = max(0, stages - S); j < stages; ++j) mbar_wait_drain(&empty[j % S], (j / S) & 1);
+    if (tiles > 0) mbar_wait_drain(acc_full, (tiles - 1) & 1);
+    if (rank == 0) {
+      for (int j = min(n0, n1); j < n; ++j) {
+        if (n0 > n1)
+          mbar_complete_tx(&full[j % S], T::kTxBytes / 2);
+        else
+          mbar_arrive_expect_tx(&full[j % S], T::kTxBytes / 2);
+      }
+      for (int j = max(0, n - S); j < n; ++j) mbar_wait_drain(&full[j % S], (j / S) & 1);
+    }
+  }
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+}
+
 // Tile t of mt x nt: bands of eight row tiles, column by column within a
 // band, so that the pairs at work share A's and B's tiles in L2.
 __device__ __forceinline__ void large_tile(int64_t t, int mt, int nt, int& m, int& n) {
@@ -516,6 +595,7 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
   uint64_t* acc_free = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* note = reinterpret_cast<volatile int*>(smem + T::kOffNote);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -531,6 +611,7 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
     mbar_init(acc_full, 1);
     mbar_init(acc_free, 16);         // the epilogue warps of both CTAs
     *abort_flag = 0;
+    note[kGaveUp] = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -548,17 +629,18 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  bool ok = true;                    // no wait of this warp has given up
   if (warp == 0) {
     // ------------------------------------------------ producer
     int i = 0;                       // stages issued so far
-    bool ok = true;
+    const int until = loads_until(p, (int)rank);
     for (int64_t t = pair; ok && t < tiles; t += pairs) {
       int mi, ni;
       large_tile(t, mt, nt, mi, ni);
       const int arow = mi * 256 + 128 * (int)rank, brow = ni * 256 + 128 * (int)rank;
       for (int s = 0; s < stages; ++s, ++i) {
         const int slot = i % T::kStages;
-        if (!(ok = warp_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status))) break;
+        if (!(ok = i < until && warp_wait(&empty[slot], ((i / T::kStages) & 1) ^ 1, abort_flag, p.status, wait_limit(p)))) break;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[slot], T::kTxBytes);
           const uint32_t bar = mapa_u32(smem_u32(&full[slot]), 0);
@@ -571,15 +653,12 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
         __syncwarp();
       }
     }
-    // nothing may reach this CTA after it ends: the slots' last releases, or
-    // after a timeout the copies in flight (which complete on the leader's
-    // barriers: long done after two milliseconds)
+    // nothing may reach this CTA after it ends: the slots' last releases (after a
+    // wait that gave up, part_after_giving_up() sees to it)
     if (ok)
-      for (int j = i > T::kStages ? i - T::kStages : 0; j < i; ++j)
-        if (!warp_wait(&empty[j % T::kStages], (j / T::kStages) & 1, abort_flag, p.status)) break;
-    if (*abort_flag)
-      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 2000000ull;) {
-      }
+      for (int j = max(0, i - T::kStages); j < i; ++j)
+        if (!(ok = warp_wait(&empty[j % T::kStages], (j / T::kStages) & 1, abort_flag, p.status, wait_limit(p)))) break;
+    if (lane == 0) note[kLoaded] = i;
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------ MMA issuer
@@ -589,14 +668,13 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
     // per stage: 1086 cycles for 512 cycles of MMAs), so the copies alone
     // halved the rate.
     constexpr uint32_t kI = Mma::idesc(256, 256);
-    int i = 0, done = 0;
-    bool ok = true;
-    for (int64_t t = pair; ok && t < tiles; t += pairs, ++done) {
+    int i = 0, done = 0;             // commits of stages and of tiles
+    for (int64_t t = pair; ok && t < tiles; t += pairs) {
       // the last tile's sums have left tensor memory
-      if (!(ok = warp_wait(acc_free, (done & 1) ^ 1, abort_flag, p.status))) break;
+      if (!(ok = warp_wait(acc_free, (done & 1) ^ 1, abort_flag, p.status, wait_limit(p)))) break;
       for (int s = 0; s < stages; ++s, ++i) {
         const int slot = i % T::kStages;
-        if (!(ok = warp_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status))) break;
+        if (!(ok = warp_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status, wait_limit(p)))) break;
         tc_fence_after();
         const uint32_t st = smem_u32(smem + slot * T::kStageBytes);
         const uint32_t tsa = tmem + T::kColSf + slot * T::kSfCols, tsb = tsa + 4 * Mma::kWords;
@@ -625,11 +703,11 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
         }
         __syncwarp();
       }
+      done += ok;
     }
-    if (!ok) {                       // MMAs in flight end before the CTA does
-      if (elect_one()) tc_commit_pair(acc_full);
-      __syncwarp();
-      mbar_wait_drain(acc_full, done & 1);
+    if (lane == 0) {
+      note[kStagesOut] = i;
+      note[kTilesOut] = done;
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -640,8 +718,7 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
     const uint32_t stage = smem_u32(smem + T::kOffOut + (warp - 4) * 4096);
     const uint32_t free_leader = mapa_u32(smem_u32(acc_free), 0);
     const bool cols = p.rb != nullptr || p.bias != nullptr;
-    int done = 0;
-    bool ok = true;                  // after a timeout the warps still meet at the barriers below
+    int done = 0;                    // (after a timeout the warps still meet at the barriers below)
     for (int64_t t = pair; t < tiles; t += pairs, ++done) {
       int mi, ni;
       large_tile(t, mt, nt, mi, ni);
@@ -655,7 +732,7 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
         bar_sync(1, 256);
       }
       const float ra = (p.ra != nullptr && row0 + lane < p.M) ? p.ra[row0 + lane] : 1.0f;
-      ok = ok && warp_wait(acc_full, done & 1, abort_flag, p.status);
+      ok = ok && warp_wait(acc_full, done & 1, abort_flag, p.status, wait_limit(p));
       if (!ok) continue;
       tc_fence_after();
       uint32_t u[4][32];
@@ -763,9 +840,11 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
     __syncwarp();
   }
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok) && threadIdx.x == 0) note_pair((int*)note + kGaveUp, 1);
   cluster_arrive();
   cluster_wait();
+  // (where all went well the last releases have been waited for)
+  if (note[kGaveUp]) part_after_giving_up<T>(note, rank, full, empty, acc_full);
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
