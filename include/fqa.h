@@ -465,7 +465,9 @@ FQA_API fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales
  * microscaled A [M, K] and B [N, K] of one format (B: weights, one row per
  * output feature), on the block-scaled tensor cores, accumulated in FP32,
  * rounded once to out_dtype; out [M, N] contiguous.  bias: FP32 [N] or NULL.
- * A row that stands for NaN gives NaN in its results only.  Results depend on
+ * Row scales may have any finite value: a result overflows or vanishes only
+ * where it lies outside binary32 itself.  A row that stands for NaN gives NaN in
+ * its results only.  Results depend on
  * the inputs, the sizes and the device's number of SMs alone (K is split in an
  * order that these fix).
  */

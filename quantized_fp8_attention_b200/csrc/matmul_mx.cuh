@@ -145,6 +145,23 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// A result is sum * ra * rb + bias, formed as fma(sum * ra, rb, bias).  Sums that are
+// not 0 lie between 2^-20 (two smallest codes under two smallest scales) and 2^43
+// (2688^2 2^20), so with ra far from 1 the first product could leave binary32
+// although rb brings the result back.  Such an ra is split into first = 2^62 or
+// 2^-62 and the rest: sum * first stays between 2^-82 and 2^105, and times rb it
+// leaves binary32 only where the rest, which is on first's side of 1, takes the
+// result further out.  fma(sum * first * rb, rest, bias) costs one more rounding.
+__device__ __forceinline__ bool far_scale(float a) {
+  const float m = fabsf(a);
+  return (m > 0.0f && m < 0x1p-80f) || (m > 0x1p80f && m <= 0x1.fffffep127f);
+}
+__device__ __forceinline__ void split_scale(float a, float& first, float& rest) {
+  const bool large = fabsf(a) > 1.0f;
+  first = large ? 0x1p62f : 0x1p-62f;
+  rest = a * (large ? 0x1p-62f : 0x1p62f);       // exact
+}
+
 struct MxMatmulParams {
   const uint8_t* sa;      // scale tiles of A [M] and B [N]
   const uint8_t* sb;
@@ -229,6 +246,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   uint64_t* done = empty + T::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* far_flag = abort_flag + 1;         // a token's row scale is far_scale()
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   const int rank = blockIdx.x % ranks, tile = blockIdx.x / ranks;
@@ -257,6 +275,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     }
     mbar_init(done, 1);
     *abort_flag = 0;
+    *far_flag = 0;
     mbar_fence_init();
     grid_wait();
     // the ring's first fill needs nothing else of the CTA
@@ -332,25 +351,41 @@ __global__ void __launch_bounds__(kMxSmallThreads)
   const int nq = min(NT, p.M - q0);                          // rows of A in the tile
   const bool scaled = p.ra != nullptr;
   float rb = 1.0f, bias = 0.0f;
+  bool far = false;
   float* ra = reinterpret_cast<float*>(smem + T::kOffRa);
   if (warp >= 2) {
     // fetched while the products run
     const int q = threadIdx.x - 64;
-    if (q < NT) ra[q] = scaled && q < nq ? p.ra[q0 + q] : 1.0f;
+    if (q < NT) {
+      ra[q] = scaled && q < nq ? p.ra[q0 + q] : 1.0f;
+      if (far_scale(ra[q])) *far_flag = 1;
+    }
     if (pr < p.N) {
       if (p.rb != nullptr) rb = p.rb[pr];
       if (p.bias != nullptr) bias = p.bias[pr];
     }
     bar_sync(1, kMxSmallThreads - 64);
+    far = *far_flag != 0;
   }
   // tokens q .. q + 3 of this thread's feature
   auto finish = [&](const float (&acc)[4], int q) {
     if (pr >= p.N) return;
     const float4 r = *reinterpret_cast<const float4*>(ra + q);
-    const float v[4] = {scaled ? fmaf(acc[0] * r.x, rb, bias) : acc[0] + bias,
-                        scaled ? fmaf(acc[1] * r.y, rb, bias) : acc[1] + bias,
-                        scaled ? fmaf(acc[2] * r.z, rb, bias) : acc[2] + bias,
-                        scaled ? fmaf(acc[3] * r.w, rb, bias) : acc[3] + bias};
+    float v[4] = {scaled ? fmaf(acc[0] * r.x, rb, bias) : acc[0] + bias,
+                  scaled ? fmaf(acc[1] * r.y, rb, bias) : acc[1] + bias,
+                  scaled ? fmaf(acc[2] * r.z, rb, bias) : acc[2] + bias,
+                  scaled ? fmaf(acc[3] * r.w, rb, bias) : acc[3] + bias};
+    if (FMT == kNvFp4 && far) {      // (512 x 4096 x 4096 10.3 -> 10.5 us, fewer rows unchanged; in a pass or
+                                     // loops of its own it cost those more)
+      const float a[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (far_scale(a[e])) {
+          float first, rest;
+          split_scale(a[e], first, rest);
+          v[e] = fmaf(acc[e] * first * rb, rest, bias);
+        }
+    }
     const size_t at = (size_t)(q0 + q) * p.N + pr;
     auto store = [&](auto* out) {
       using O = std::remove_pointer_t<decltype(out)>;
@@ -744,9 +779,25 @@ __global__ void __launch_bounds__(kMxLargeThreads, 1)
       if (lane == 0) mbar_arrive_cluster(free_leader);
       const float* rb = sc + 128 * half;
       const float* bias = rb + 256;
+      if (FMT == kNvFp4 && far_scale(ra)) {
+        // (through local memory, 32 sums at a time: unrolled it cost the loop around
+        // it spills)
+        float first, rest;
+        split_scale(ra, first, rest);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (cols) {
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = u[c][e];
+#pragma unroll 1
+          for (int e = 0; e < 32; ++e)
+            w[e] = __float_as_uint(fmaf(__uint_as_float(w[e]) * first * rb[32 * c + e], rest, bias[32 * c + e]));
+#pragma unroll
+          for (int e = 0; e < 32; ++e) u[c][e] = w[e];
+        }
+      } else if (cols) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 f = *reinterpret_cast<const float4*>(rb + 32 * c + e);
