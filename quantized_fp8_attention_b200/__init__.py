@@ -696,9 +696,11 @@ def _mx_format(fmt) -> int:
     return code
 
 
-@functools.lru_cache(maxsize=1024)
+@functools.lru_cache(maxsize=1024, typed=True)
 def _mx_shapes(M: int, K: int, code: int):
     """Shapes of the codes and of the scale tiles of [M, K]."""
+    if not isinstance(M, int) or not isinstance(K, int):
+        raise ValueError(f"[{M!r}, {K!r}]: expected whole numbers of rows and values")
     if not 0 <= M <= _MX_MAX_ROWS or not 1 <= K <= _MX_MAX_COLS:
         raise ValueError(f"[{M}, {K}]: microscaled rows are at most 2^24, of 1 to 2^20 values")
     kp = (K + 31) // 32 * 32
@@ -905,9 +907,16 @@ class Rotary(NamedTuple):
     eps: float = 1e-6
 
 
-@functools.lru_cache(maxsize=64)
 def _axes_array(axes: tuple, split: bool):
-    if not 1 <= len(axes) <= 4 or any(not isinstance(a, int) or a < 2 or a % 2 for a in axes) or sum(axes) > HEAD_DIM:
+    # (types here: the cache takes 64.0 for 64)
+    if any(not isinstance(a, int) for a in axes):
+        raise ValueError(f"axes: expected whole channel counts, got {axes}")
+    return _axes_of(axes, split)
+
+
+@functools.lru_cache(maxsize=64)
+def _axes_of(axes: tuple, split: bool):
+    if not 1 <= len(axes) <= 4 or any(a < 2 or a % 2 for a in axes) or sum(axes) > HEAD_DIM:
         raise ValueError(f"axes: expected one to four even channel counts, together at most {HEAD_DIM}, got {axes}")
     if split and sum(axes) % 16:
         raise ValueError(f"axes: split pairs need a multiple of 16 channels, got {sum(axes)}")
