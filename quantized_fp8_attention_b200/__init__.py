@@ -760,9 +760,9 @@ def _rows(x, name: str):
 def _require_mx_out(out, fmt: str, M: int, K: int, code: int, index: int, inputs) -> None:
     if _require_microscaled(out, "out", index)[:2] != (M, code) or out.cols != K:
         raise ValueError(f"out: expected {fmt} rows [{M}, {K}]")
-    for t in out[:3]:
-        if t is not None:
-            _apart(t, "out", inputs)
+    parts = [t for t in out[:3] if t is not None]
+    for i, t in enumerate(parts):
+        _apart(t, "out", (*inputs, *parts[:i]))
 
 
 def mx_quantize(x: torch.Tensor, fmt: str, out: Optional[Microscaled] = None, stream=None) -> Microscaled:
