@@ -308,9 +308,8 @@ __global__ void __launch_bounds__(kMxSmallThreads)
     }
   } else if (warp == 1) {
     constexpr uint32_t kI = Mma::idesc(128, NT);
-    // the Q tile's place in its block of 128 rows: 32 rows per column (a tile of
-    // 16 rows is only taken where it is the only one, at row 0)
-    const uint32_t qcol = (uint32_t)(q0 % 128) / 32;
+    // (a tile starts a block of 128 rows of scales: those of fewer tokens are only
+    // taken where they are the only one)
     for (int s = s0; s < s1; ++s) {
       const int i = s - s0, slot = i % T::kStages;
       if (!warp_wait(&full[slot], (i / T::kStages) & 1, abort_flag, p.status, wait_limit(p))) break;
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(kMxSmallThreads)
           if (kk >= left) break;
           const uint32_t ids = (Mma::sf_id(kk) << 4) | (Mma::sf_id(kk) << 29);
           mma_mx<FMT, 1>(tmem, dP + 2 * kk, dQ + 2 * kk, kI | ids, tsp + 4 * Mma::word(kk),
-                         tsq + 4 * Mma::word(kk) + qcol, s > s0 || kk > 0);
+                         tsq + 4 * Mma::word(kk), s > s0 || kk > 0);
         }
         tc_commit(&empty[slot]);
       }

@@ -89,47 +89,10 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// W consecutive elements (W * sizeof(T) a multiple of 8 bytes) as binary32;
-// the address is aligned to min(16, W * sizeof(T)) bytes.
-template <typename T, int W>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[W]) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const float4 f = reinterpret_cast<const float4*>(p)[i];
-      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-    }
-  } else {
-    uint32_t w[W / 2];
-    if constexpr (W == 8) {
-      const uint4 r = *reinterpret_cast<const uint4*>(p);
-      w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
-    } else {
-      static_assert(W == 4, "four or eight elements");
-      const uint2 r = *reinterpret_cast<const uint2*>(p);
-      w[0] = r.x; w[1] = r.y;
-    }
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      const float2 f = unpack2<T>(w[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
-template <typename T, int W>
-__device__ __forceinline__ void store_vec(T* p, const float (&v)[W]) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i)
-      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  } else if constexpr (W == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
-                                              pack2<T>(v[6], v[7]));
-  } else {
-    static_assert(W == 4, "four or eight elements");
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-  }
+// Four neighbours of a 16-bit type on an 8-byte boundary.
+template <typename T>
+__device__ __forceinline__ void store_four(T* p, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
 }
 
 // 32 bytes per thread in one access (sm_100; address on a 32-byte boundary):
@@ -886,7 +849,7 @@ __global__ void __launch_bounds__(256) mx_dequantize_any_kernel(const MxDequantP
         v[2 * e + 1] = FMT == kNvFp4 ? f.y * s * rs : f.y * s;
       }
       if constexpr (W == 4) {
-        store_vec<T, 4>(out + 4 * c, v);
+        store_four(out + 4 * c, v);
       } else if (p.wide) {
         MxFew<T, 2>::store(out + 2 * c, v);
       } else {
