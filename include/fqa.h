@@ -446,6 +446,11 @@ FQA_API fqa_status fqa_mx_quantize(const void* x, fqa_dtype dtype, int M, int K,
  * x's type; residual_out is contiguous [M, K] and given exactly when residual
  * is; it may be the residual itself (then ldr = K), or x where types and
  * strides agree, and overlap nothing else.  eps >= 0.
+ * The squares are summed in FP32.  A finite row whose sum of squares overflows
+ * there (beyond 2^128: values of 2^64 / sqrt(K), about 3e17 at K = 4096) gives
+ * y = 0; with eps = 0, values below about 1e-19 lose accuracy in their squares,
+ * and where these vanish y is infinite or NaN.  An infinity in h makes its own y NaN and the row's others
+ * 0, a NaN the whole row NaN (as blocks or rows then stand for NaN).
  */
 FQA_API fqa_status fqa_mx_rms_norm(const void* x, fqa_dtype dtype, int M, int K, int64_t ldx, const void* weight,
                                    fqa_dtype weight_dtype, float eps, const void* residual,
@@ -467,9 +472,8 @@ FQA_API fqa_status fqa_mx_dequantize(const uint8_t* codes, const uint8_t* scales
  * rounded once to out_dtype; out [M, N] contiguous.  bias: FP32 [N] or NULL.
  * Row scales may have any finite value: a result overflows or vanishes only
  * where it lies outside binary32 itself.  A row that stands for NaN gives NaN in
- * its results only.  Results depend on
- * the inputs, the sizes and the device's number of SMs alone (K is split in an
- * order that these fix).
+ * its results only.  Results depend on the inputs, the sizes and the device's
+ * number of SMs alone (K is split in an order that these fix).
  */
 FQA_API fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_row_scale,
                                  const uint8_t* b_codes, const uint8_t* b_scales, const float* b_row_scale,
@@ -491,7 +495,10 @@ FQA_API fqa_status fqa_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales
  *     the i-th pair of its axis, or 2 j / D with FQA_ROTARY_SHARED
  *   (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos), rounded once
  *   norm: x / sqrt(mean of x^2 over the head's 128 channels + eps) * weight[128]
- *     (of Q's type) before the rotation; NULL: none
+ *     (of Q's type) before the rotation, the squares summed in FP32 (a head
+ *     whose sum of squares is beyond 2^128 gives 0); NULL: none
+ * A non-finite channel makes its own pair non-finite; with a norm an infinity
+ * makes its pair NaN and the head's other channels 0, a NaN the head NaN.
  * q, k       strides of batch, head and token in elements, channels adjacent
  *            (a view of a packed projection will do); either may have no
  *            heads.  Rows on 16-byte boundaries load in vectors.

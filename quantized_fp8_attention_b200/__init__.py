@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(_PKG, "libfqa.so")
 
 FQA_OK, FQA_ERR_INVALID_ARG, FQA_ERR_UNSUPPORTED, FQA_ERR_MISALIGNED, FQA_ERR_CUDA, FQA_ERR_TIMEOUT = range(6)
 FQA_OUT_BF16, FQA_OUT_F32 = 0, 1
-FQA_OUT_F16 = 2            # mx_matmul and mx_dequantize only
+FQA_OUT_F16 = 2            # mx_matmul and mx_dequantize only: the attention calls refuse it
 HEAD_DIM = 128
 
 _lib = None
@@ -515,7 +515,8 @@ def attention_fp8_corrected(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q
 def fp8_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_scale: float,
                   out_dtype: int = FQA_OUT_BF16, stream=None, rot: Optional["Rotary"] = None) -> torch.Tensor:
     """The whole FP8 path: with rot, rotary() on q and k (which may then be
-    strided views); quantize; fused FP8 attention."""
+    strided views; as many heads as v, which is contiguous); quantize; fused FP8
+    attention."""
     if rot is not None:
         q, k = rotary(q, k, rot, stream=stream)
     return attention_fp8(quantize(q, k, v, stream=stream), softmax_scale, out_dtype, stream=stream)
@@ -607,6 +608,11 @@ def e2m1_encode(x: torch.Tensor, stream=None) -> torch.Tensor:
 
 
 # ------------------------------------- rotary positions, microscaled rows
+#
+# Each function first tries csrc/binding.cpp, which takes the everyday call: no
+# output or stream given, tensors on the current device, eps and theta floats, axes
+# a tuple, split, shared and inverse truth values.  Any other call costs 10 to 15 us
+# more on the host.
 
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2, torch.int32: 3}
 _OUT_DTYPE = {FQA_OUT_BF16: torch.bfloat16, FQA_OUT_F32: torch.float32, FQA_OUT_F16: torch.float16}

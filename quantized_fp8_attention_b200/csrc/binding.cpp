@@ -1,12 +1,14 @@
 // binding.cpp -- the short way into the calls around the attention: the checks
 // and allocations of __init__.py's functions for the everyday call (no output
-// given, tensors on the current device, current stream), without the
-// interpreter.  A call that is anything else, or that the library refuses,
+// or stream given, tensors on the current device; eps and theta floats, axes a
+// tuple, flags truth values), without the interpreter.  A call that is anything else, or that the library refuses,
 // answers None, and the Python function of the same name goes through its
 // checks and says what is wrong; so every rule is stated there, and this file
 // may only accept what it would accept.
 //
-// At one token the kernels take 3 to 6 us and the Python way 10 to 19.
+// At one token the kernels take 2 to 5 us, this way 3.5 to 6 and the Python way
+// 14 to 19.  Where this file is not built, or built for another torch or Python,
+// the Python way serves alone (__init__.py, _CheckedWay).
 #include <Python.h>
 
 #include <dlfcn.h>

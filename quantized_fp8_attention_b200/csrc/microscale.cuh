@@ -619,7 +619,9 @@ __device__ __forceinline__ int mx_any_place(int e) { return e ^ (((e >> 5) & 3) 
 // CTAs per SM that the registers have to allow.  16-bit pairs with a norm: five
 // (four by themselves; 8704 x 4098 BF16 to mxfp8 67 -> 60 us; FP32 pairs would
 // spill, 1023 x 5102: 17 -> 21 us, and single values lose 6% for nvfp4).  Without
-// a norm: six (12288 x 4097 BF16 to mxfp4 56 -> 53 us; FP32 pairs 48 -> 51 us).
+// a norm: six (12288 x 4097 BF16 to mxfp4 56 -> 53 us, although mxfp8 and mxfp4
+// spill 36 bytes for it, single values of every type and 16-bit pairs; FP32 pairs
+// 48 -> 51 us).
 template <typename T, bool kNorm, int E>
 constexpr int mx_any_ctas() {
   if (E == 2 && sizeof(T) == 4) return 0;      // as the compiler likes
