@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import warnings
 from typing import NamedTuple, Optional
@@ -705,8 +706,10 @@ def _mx_format(fmt) -> int:
 @functools.lru_cache(maxsize=1024, typed=True)
 def _mx_shapes(M: int, K: int, code: int):
     """Shapes of the codes and of the scale tiles of [M, K]."""
-    if not isinstance(M, int) or not isinstance(K, int):
-        raise ValueError(f"[{M!r}, {K!r}]: expected whole numbers of rows and values")
+    try:
+        M, K = operator.index(M), operator.index(K)
+    except TypeError:
+        raise ValueError(f"[{M!r}, {K!r}]: expected whole numbers of rows and values") from None
     if not 0 <= M <= _MX_MAX_ROWS or not 1 <= K <= _MX_MAX_COLS:
         raise ValueError(f"[{M}, {K}]: microscaled rows are at most 2^24, of 1 to 2^20 values")
     kp = (K + 31) // 32 * 32
@@ -719,7 +722,7 @@ def alloc_microscaled(M: int, K: int, fmt: str, device) -> Microscaled:
     codes, scales = _mx_shapes(M, K, code)
     return Microscaled(torch.empty(codes, dtype=torch.uint8, device=device),
                        torch.empty(scales, dtype=torch.uint8, device=device),
-                       torch.empty(M, dtype=torch.float32, device=device) if code == 2 else None, K, fmt)
+                       torch.empty(M, dtype=torch.float32, device=device) if code == 2 else None, operator.index(K), fmt)
 
 
 def _require_microscaled(q, name: str, index: int = -1):

@@ -25,3 +25,9 @@ def test_a_float_is_refused_whatever_was_asked_before_and_spoils_nothing_after()
                     fqa._axes_array(axes, False)
             else:
                 assert list(fqa._axes_array(axes, False)) == list(axes)
+
+
+def test_whole_numbers_of_other_types_serve():
+    np = pytest.importorskip("numpy")
+    q = fqa.alloc_microscaled(np.int64(130), np.int32(100), "nvfp4", "cpu")
+    assert q.codes.shape == (130, 64) and q.scales.shape == (2, 2, 32, 4, 4) and type(q.cols) is int and q.cols == 100
