@@ -309,8 +309,12 @@ def fqa_debug_mx_matmul_timeout(a: "Microscaled", b: "Microscaled", out: torch.T
     P, I = ctypes.c_void_p, ctypes.c_int
     L.fqa_debug_mx_matmul_timeout.restype = I
     L.fqa_debug_mx_matmul_timeout.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, I, I, I, P]
-    M, code, _ = _require_microscaled(a, "a")
-    N = _require_microscaled(b, "b")[0]
+    M, code, index = _require_microscaled(a, "a")
+    N, other, _ = _require_microscaled(b, "b", index)
+    if other != code or a.cols != b.cols:
+        raise ValueError(f"a and b: {a.fmt} rows of {a.cols} against {b.fmt} rows of {b.cols}")
+    _device_tensor(out, "out", index)
+    _require(out, _OUT_DTYPE[out_dtype], "out", (M, N))
     return L.fqa_debug_mx_matmul_timeout(_ptr(a.codes), _ptr(a.scales), _ptr(a.row_scale), _ptr(b.codes), _ptr(b.scales),
                                          _ptr(b.row_scale), None, M, N, a.cols, code, _ptr(out), int(out_dtype),
                                          int(rank), int(stage), _stream(stream))
